@@ -17,6 +17,8 @@
 #include "tq4_prefill.cuh"
 #include "tq4_prefill_tc.cuh"
 #include "tq4_decode_tc.cuh"
+#include "tq4_decode_window.cuh"
+#include "tq4_step.cuh"
 
 struct tq4_ctx {
   int device;
@@ -430,6 +432,9 @@ int tq4_ctx_create(const int8_t* signs, tq4_ctx** out) {
   if (e == cudaSuccess) e = set_decode_attrs<2, 2, true>();
   if (e == cudaSuccess) e = set_decode_attrs<3, 3, true>();
   if (e == cudaSuccess) e = tq4::prefill_tc_set_attrs();
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(tq4::g_boundaries64, ctx->boundaries, sizeof(ctx->boundaries));
+  if (e == cudaSuccess) e = tq4::plan_set_attrs();
+  if (e == cudaSuccess) e = tq4::window_set_attrs();
   if (e == cudaSuccess) e = set_decode_tc_attrs<2>();
   if (e == cudaSuccess) e = set_decode_tc_attrs<3>();
   if (e == cudaSuccess) e = cudaGetSymbolAddress(&ctx->noalloc_scratch, g_noalloc_scratch);
@@ -824,6 +829,164 @@ int tq4_tqb_prefill_attention(tq4_ctx* ctx, int bits, const void* pool, int32_t 
   if (bits != 2 && bits != 3) return ctx ? TQ4_ERR_UNSUPPORTED : TQ4_ERR_ARG;
   return prefill_impl(ctx, pool, num_pages, page_table, table_len, prefix_len, q, k_chunk, v_chunk, n_tok, scale, out,
                       out_dtype, workspace, workspace_bytes, stream, true, bits);
+}
+
+// ---------------------------------------------------------------------------
+// The ragged serving step: plan, rotary append by slot, windowed decode.
+// ---------------------------------------------------------------------------
+int tq4_plan_step(tq4_ctx* ctx, const int32_t* past_lens, const int32_t* new_lens, int32_t n_req,
+                  const int32_t* free_pages, int32_t n_free, int32_t num_pages, int32_t* page_tables,
+                  int32_t max_pages, int32_t* cu_tok, int32_t* seq_lens, int32_t* tok_pos, int64_t* tok_slot,
+                  int32_t max_tok, int32_t* taken, void* stream) {
+  if (!ctx || n_req < 0 || n_free < 0 || max_tok < 0 || max_pages <= 0 || num_pages <= 0) return TQ4_ERR_ARG;
+  if (n_req > TQ4_PLAN_MAX_REQUESTS || int64_t(max_pages) * tq4::kPage > INT32_MAX) return TQ4_ERR_UNSUPPORTED;
+  if (!cu_tok || !taken || (n_req > 0 && (!past_lens || !new_lens || !page_tables || !seq_lens)) ||
+      (n_free > 0 && !free_pages) || (max_tok > 0 && (!tok_pos || !tok_slot)))
+    return TQ4_ERR_ARG;
+  if (!aligned(tok_slot, 8)) return TQ4_ERR_ARG;
+  if (int rc = check_device(ctx)) return rc;
+  tq4::PlanParams p{past_lens, new_lens, n_req,    free_pages, n_free,   num_pages, page_tables, max_pages,
+                    cu_tok,    seq_lens, tok_pos,  tok_slot,   max_tok,  taken,     ctx->d_status};
+  return cuda_status(tq4::launch_plan_step(p, ctx->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int tq4_rope_table(tq4_ctx* ctx, float* table, int32_t table_len, int32_t rot, double base, void* stream) {
+  if (!ctx || table_len < 0) return TQ4_ERR_ARG;
+  if (rot < 16 || rot > tq4::kD || rot % 16 != 0) return TQ4_ERR_UNSUPPORTED;
+  if (!std::isfinite(base) || !(base > 0.0)) return TQ4_ERR_ARG;
+  if (table_len == 0) return TQ4_OK;
+  if (!table || !aligned(table, 16)) return TQ4_ERR_ARG;
+  if (int rc = check_device(ctx)) return rc;
+  return cuda_status(tq4::launch_rope_table(reinterpret_cast<float2*>(table), table_len, rot, base,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+int tq4_rope_append(tq4_ctx* ctx, void* pool, int32_t num_pages, const void* q, const void* k, const void* v,
+                    int dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride, int32_t n_tok,
+                    const int32_t* pos, int32_t n_axes, const int32_t* sections, int interleaved, int adjacent_pairs,
+                    const float* table, int32_t table_len, int32_t rot, const int64_t* slots, uint16_t* q_out,
+                    uint16_t* k_out, void* stream) {
+  if (!ctx || n_tok < 0) return TQ4_ERR_ARG;
+  if (n_axes < 1 || n_axes > TQ4_ROPE_MAX_AXES || rot < 16 || rot > tq4::kD || rot % 16 != 0)
+    return TQ4_ERR_UNSUPPORTED;
+  if (dtype != TQ4_DTYPE_F32 && dtype != TQ4_DTYPE_BF16) return TQ4_ERR_ARG;
+  if (!sections) return TQ4_ERR_ARG;
+  // the axis of each frequency: axes in blocks of their sections, or dealt out in turn
+  // (frequency i goes to axis i mod n_axes while i < n_axes * sections[axis], else to axis 0)
+  const int half = rot / 2;
+  int64_t sum = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    if (sections[a] < 0) return TQ4_ERR_ARG;
+    sum += sections[a];
+  }
+  if (sum != half) return TQ4_ERR_ARG;
+  tq4::RopeParams p{};
+  int dealt[TQ4_ROPE_MAX_AXES] = {};
+  for (int i = 0, block = 0, end = sections[0]; i < half; ++i) {
+    int a;
+    if (interleaved) {
+      a = i % n_axes;
+      if (i >= n_axes * sections[a]) a = 0;
+    } else {
+      while (i >= end) end += sections[++block];
+      a = block;
+    }
+    ++dealt[a];
+    p.axis[i >> 4] |= uint32_t(a) << (2 * (i & 15));
+  }
+  for (int a = 0; a < n_axes; ++a)
+    if (dealt[a] != sections[a]) return TQ4_ERR_ARG;   // these sections cannot be dealt out in turn
+  if (n_tok == 0) return TQ4_OK;
+  if (!pool || num_pages <= 0 || !k || !v || !pos || !table || table_len <= 0 || !slots || (q == nullptr) != (q_out == nullptr))
+    return TQ4_ERR_ARG;
+  const int64_t size = dtype == TQ4_DTYPE_F32 ? 4 : 2;
+  if (k_stride < tq4::kHkv * tq4::kD || v_stride < tq4::kHkv * tq4::kD || (q && q_stride < tq4::kHq * tq4::kD))
+    return TQ4_ERR_ARG;
+  if ((k_stride * size) % 16 || (v_stride * size) % 16 || (q && (q_stride * size) % 16)) return TQ4_ERR_ARG;
+  if (!aligned(pool, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(table, 16) ||
+      !aligned(slots, 8) || !aligned(q_out, 16) || !aligned(k_out, 16))
+    return TQ4_ERR_ARG;
+  if (int rc = check_device(ctx)) return rc;
+  p.pool = static_cast<uint8_t*>(pool);
+  p.num_pages = num_pages;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.n_tok = n_tok;
+  p.pos = pos;
+  p.n_axes = n_axes;
+  p.table = reinterpret_cast<const float2*>(table);
+  p.table_len = table_len;
+  p.rot = rot;
+  p.adjacent = adjacent_pairs ? 1 : 0;
+  p.slots = slots;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.signs = ctx->signs;
+  p.status = ctx->d_status;
+  return cuda_status(tq4::launch_rope_append(p, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int tq4_reconstruct_slots(tq4_ctx* ctx, const void* pool, int32_t num_pages, const int64_t* slots, int32_t n,
+                          void* k_out, void* v_out, int out_dtype, void* stream) {
+  if (!ctx || n < 0) return TQ4_ERR_ARG;
+  if (out_dtype != TQ4_DTYPE_F32 && out_dtype != TQ4_DTYPE_BF16) return TQ4_ERR_ARG;
+  if (n == 0) return TQ4_OK;
+  if (!pool || !slots || !k_out || !v_out || num_pages <= 0) return TQ4_ERR_ARG;
+  if (!aligned(pool, 16) || !aligned(slots, 8) || !aligned(k_out, 16) || !aligned(v_out, 16)) return TQ4_ERR_ARG;
+  if (int rc = check_device(ctx)) return rc;
+  return cuda_status(tq4::launch_reconstruct_slots(static_cast<const uint8_t*>(pool), num_pages, slots, n, k_out, v_out,
+                                                   out_dtype, ctx->signs, ctx->d_status,
+                                                   static_cast<cudaStream_t>(stream)));
+}
+
+size_t tq4_decode_window_workspace_bytes(const tq4_ctx* ctx, int32_t n_req, int32_t n_q, int32_t max_pages,
+                                         int32_t window, int32_t n_sink) {
+  if (!ctx || n_req <= 0 || n_q < 1 || n_q > TQ4_MAX_QUERY_TOKENS || max_pages <= 0 || window < 1 || n_sink < 0) return 0;
+  return tq4::window_workspace_bytes(ctx->num_sms, n_req, n_q, max_pages, window, n_sink);
+}
+
+int tq4_decode_attention_window(tq4_ctx* ctx, const void* pool, int32_t num_pages, const uint16_t* q,
+                                const int32_t* page_tables, int32_t max_pages, const int32_t* seq_lens, int32_t n_req,
+                                int32_t n_q, int32_t window, int32_t n_sink, float scale, void* out, int out_dtype,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  if (!ctx || n_req < 0) return TQ4_ERR_ARG;
+  if (n_q < 1 || n_q > TQ4_MAX_QUERY_TOKENS) return TQ4_ERR_UNSUPPORTED;
+  if (window < 1 || n_sink < 0 || !std::isfinite(scale)) return TQ4_ERR_ARG;
+  if (out_dtype != TQ4_DTYPE_F32 && out_dtype != TQ4_DTYPE_BF16) return TQ4_ERR_ARG;
+  if (n_req == 0) return TQ4_OK;
+  if (!pool || !q || !page_tables || !seq_lens || !out || num_pages <= 0 || max_pages <= 0) return TQ4_ERR_ARG;
+  if (!aligned(pool, 16) || !aligned(q, 16) || !aligned(out, 16)) return TQ4_ERR_ARG;
+  if (int64_t(max_pages) * tq4::kPage > INT32_MAX || int64_t(num_pages) * tq4::kRowsPerPage > INT32_MAX)
+    return TQ4_ERR_UNSUPPORTED;
+  const size_t need = tq4::window_workspace_bytes(ctx->num_sms, n_req, n_q, max_pages, window, n_sink);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return TQ4_ERR_WORKSPACE;
+  if (int rc = check_device(ctx)) return rc;
+  CUtensorMap map;
+  if (int rc = pool_tensor_map(pool, num_pages, &map)) return rc;
+  tq4::WindowParams p{};
+  p.pool = static_cast<const uint8_t*>(pool);
+  p.num_pages = num_pages;
+  p.q = q;
+  p.tables = page_tables;
+  p.max_pages = max_pages;
+  p.seq_lens = seq_lens;
+  p.n_req = n_req;
+  p.n_q = n_q;
+  p.window = window;
+  p.n_sink = n_sink;
+  p.scale = scale;
+  p.splits = tq4::window_splits(ctx->num_sms, n_req, n_q, max_pages, window, n_sink);
+  p.out = out;
+  p.out_dtype = out_dtype;
+  p.signs = ctx->signs;
+  p.status = ctx->d_status;
+  p.spin_limit = ctx->wait_polls;
+  p.test_withhold = ctx->withhold;
+  return cuda_status(tq4::launch_decode_window(p, map, static_cast<cudaStream_t>(stream)));
 }
 
 int tq4_get_status(tq4_ctx* ctx, void* stream) {

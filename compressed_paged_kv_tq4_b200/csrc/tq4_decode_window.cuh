@@ -1,0 +1,793 @@
+// TQ4 decode attention with a sliding window and sinks, 1-4 query tokens (sm_100a).
+//
+// Query token t of a request stands at position P = seq_len - n_q + t and sees the
+// positions j <= P with j > P - window or j < n_sink. The arithmetic is the rotated-
+// domain attention of the split-K decode ([KVEXEC] simpleprog.com "Fitting a
+// 27B-Parameter LLM into 24 GiB of Laptop Memory", section "KVExec"; [V2] wpnews.pro
+// "JustFit: Run Qwen 27B Fast ...", mechanism table row KVExec):
+//   s_j = n_j (R q) . c[idx_j] * scale,  o = R^T sum_j p_j n_j c[idx_j] / sum_j p_j.
+//
+// Work split. Only the 32-position tiles that some query token sees are visited: those
+// of the sinks, then those of the window. A cluster of CS CTAs owns one (request, KV
+// head); its 8 CS warps take the visible tiles in turn, each through its own two-stage
+// TMA ring, and the partial results meet in shared memory, first in the CTA, then over
+// the cluster's distributed shared memory, where each output row is merged, rotated
+// back and stored by one warp. So the call is one launch and needs no workspace: a
+// window bounds the work per request, and the second launch of a split-K scheme
+// (~3.5 us) would cost as much as the window itself.
+//
+// One token (NT = 1 n-tile: 6 query heads padded to 8): a warp keeps all 256 dims of
+// its rows' sums in registers. 2-4 tokens (NT = 2, 3): those would be 128-192 registers,
+// so warps work in pairs: each scores its own tile (K phase), the pair agrees on the
+// rows' running maxima and exchanges its weights through shared memory (in the K words
+// that both have finished with), and each sums half of the dims over both tiles.
+//
+// Operands. bf16 results: q', the centroids and the weights enter the tensor cores as
+// single f16 values (each off by at most 2^-11 relative; in the result these are
+// ~6e-4 next to the 1.7e-3 of the bf16 rounding itself, both root mean square). fp32
+// results (kExact): f16 hi + lo pairs, S = C q'hi + C q'lo + R q'hi, O = C Phi + C Plo
+// + R Phi, with the weights at most 1 so that their lo parts keep their digits.
+#pragma once
+#include "tq4_decode_q1.cuh"
+
+namespace tq4 {
+
+struct WindowParams {
+  const uint8_t* pool;
+  int32_t num_pages;
+  const uint16_t* q;
+  const int32_t* tables;
+  int32_t max_pages;
+  const int32_t* seq_lens;
+  int32_t n_req;
+  int32_t n_q;
+  int32_t window;
+  int32_t n_sink;
+  float scale;
+  int32_t splits;        // CTAs per (request, KV head) = cluster size
+  void* out;
+  int out_dtype;
+  Signs signs;
+  int* status;
+  uint32_t spin_limit;
+  int test_withhold;
+};
+
+constexpr int kWdMaxCluster = 8;
+// Shared memory: control, q' hi and lo, barriers, norm rows and maxima, then 4 tile
+// buffers below the centroid table (at kQ1Lut, as in the one-token kernel) and 12 above.
+constexpr uint32_t kWdFacOff = 128;                                     // row factors, f32 [24]
+constexpr uint32_t kWdMaxOff = kWdFacOff + 128;                         // maxima, then m and l: f32 [2][8 warps][24]
+constexpr uint32_t kWdBarOff = kWdMaxOff + 2 * 8 * 24 * 4;
+constexpr uint32_t kWdNrmOff = kWdBarOff + 128;
+constexpr uint32_t kWdQvOff = kWdNrmOff + kQ1Bufs * 128;
+constexpr uint32_t kWdCtlBytes = kWdQvOff + 2 * 24 * kQvStride * 2;     // 29,184
+constexpr int kWdLowBufs = 4;
+constexpr uint32_t kWdDynBytes = kQ1Hi + (kQ1Bufs - kWdLowBufs) * kQ1Buf;
+static_assert(kWdDynBytes <= 227 * 1024 && kWdQvOff % 16 == 0, "shared memory");
+constexpr int kWdPitch = kD + 4;                                         // floats per merged row
+template <int NT>
+constexpr int wd_slabs() { return NT == 1 ? kQ1Warps : 2; }
+static_assert(8 * 8 * kWdPitch * 4 <= (kQ1Bufs - kWdLowBufs) * kQ1Buf && 2 * 24 * kWdPitch * 4 <= 8 * 8 * kWdPitch * 4,
+              "merge rows fit above the table");
+// P' = p * n_v / 16 with p <= 2^4 (bf16 results; the reference is raised only when a row's
+// maximum grows by more), P' = p * n_v with p <= 1 (fp32): at most 65,504 either way.
+template <bool kExact>
+constexpr float wd_lazy() { return kExact ? 0.f : 4.f; }
+template <bool kExact>
+constexpr float wd_pscale() { return kExact ? 1.f : 0.0625f; }
+
+__device__ __forceinline__ uint2 ld_shared_v2u(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void pair_sync(int pair) {   // the two warps of a pair
+  asm volatile("bar.sync %0, 64;\n" ::"r"(pair + 1) : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t wd_map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void wd_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+
+// One output row: o = R^T acc / l, stored by one warp (lane: dims 8 lane ..).
+__device__ __forceinline__ void wd_store_row(const WindowParams& p, int64_t row, float acc[8], float inv, uint32_t sb) {
+  const int lane = threadIdx.x & 31;
+  warp_fwht256(acc);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = apply_sign(acc[i] * inv, sb, i);
+  const int64_t off = row * kD + lane * 8;
+  if (p.out_dtype == TQ4_DTYPE_F32) {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + off);
+    dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+  } else {
+    uint32_t pk[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b2 = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
+      pk[i] = *reinterpret_cast<const uint32_t*>(&b2);
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + off) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+  }
+}
+
+template <int NT, bool kExact>
+__global__ void __launch_bounds__(kQ1Threads, 1)
+    decode_window_kernel(const WindowParams p, const __grid_constant__ CUtensorMap tmap) {
+  constexpr bool kPair = NT > 1;
+  constexpr int kMT = kPair ? 8 : 16;            // m-tiles of dims that a warp sums
+  constexpr int kRows = 8 * NT;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int h = blockIdx.y;
+  const int r = int(blockIdx.x) / p.splits, rank = int(blockIdx.x) % p.splits;
+  // in a cluster, rank r's own shared addresses start at r << 24: the layout's fixed offsets are
+  // taken from there (lut_lo and hi_buf below are shared addresses of this CTA)
+  const uint32_t win = base & 0xFF000000u;
+  const uint32_t lut_lo = win | kQ1Lut, hi_buf = win | kQ1Hi;
+  const uint32_t low0 = (base + kWdCtlBytes + 1023) & ~1023u;
+  if (low0 + kWdLowBufs * kQ1Buf > lut_lo) {   // the layout needs the dynamic window to start low
+    if (tid == 0) record_error(p.status, TQ4_ERR_CUDA);
+    if (p.splits > 1) {   // the others of the cluster may be at work: keep their barriers and this memory alive
+      wd_cluster_sync();
+      wd_cluster_sync();
+    }
+    return;
+  }
+  float* const row_fac = reinterpret_cast<float*>(smem + kWdFacOff);
+  float* const mx_s = reinterpret_cast<float*>(smem + kWdMaxOff);        // [8][24]
+  float* const l_s = mx_s + 8 * 24;                                        // [8][24]
+  __half* const qv_hi = reinterpret_cast<__half*>(smem + kWdQvOff);
+  __half* const qv_lo = qv_hi + 24 * kQvStride;
+  auto buf_addr = [&](int b) { return b < kWdLowBufs ? low0 + b * kQ1Buf : hi_buf + (b - kWdLowBufs) * kQ1Buf; };
+  const uint32_t lanebase = lut_lo | (uint32_t(lane) * 4u);
+
+  // prologue that reads none of the call's inputs
+  if (tid < kQ1Bufs) mbar_init(base + kWdBarOff + tid * 8, 1);
+  asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  // table rows: 32 copies of the c16 pair, then (fp32 results) 32 copies of the r16 pair
+  for (int e = tid; e < 256 * (kExact ? 16 : 8); e += kQ1Threads) {
+    const int b = kExact ? e >> 4 : e >> 3, c = kExact ? e & 15 : e & 7;
+    const uint2 v = lut_row(b);
+    const uint32_t x = (c & 8) ? v.y : v.x;
+    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(lut_lo + b * 256 + c * 16), "r"(x) : "memory");
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const int n_rows = kGroup * p.n_q;
+  const int T = __ldg(p.seq_lens + r);
+  const uint32_t sb = lane_sign_bits(p.signs);
+  const int64_t out_row0 = int64_t(r) * p.n_q * kHq + h * kGroup;   // + token * 24 + head
+  if (T < p.n_q || int64_t(T) > int64_t(p.max_pages) * kPage) {   // a padded request (0), or a bad length
+    if (rank == 0) {
+      if (T != 0 && tid == 0) record_error(p.status, TQ4_ERR_SEQ);
+      for (int row = w; row < n_rows; row += kQ1Warps) {
+        float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        wd_store_row(p, out_row0 + (row / kGroup) * kHq + row % kGroup, z, 0.f, 0u);
+      }
+    }
+    return;   // the same in every CTA of the cluster
+  }
+  const int first = T - p.n_q;                                // position of query token 0
+  const int lo = max(0, first - p.window + 1);                // first position inside a window
+  const int a_t = (min(p.n_sink, lo) + kQ1Tile - 1) / kQ1Tile;   // sink tiles
+  const int skip = max(lo / kQ1Tile - a_t, 0);                // tiles between the sinks and the window
+  const int n_tiles = (T + kQ1Tile - 1) / kQ1Tile - skip;
+  const int32_t* const table = p.tables + int64_t(r) * p.max_pages;
+  // visible tile i (in order) -> its first position; tile k of this warp
+  auto tile_pos = [&](int k) {
+    const int i = (k * p.splits + rank) * kQ1Warps + w;
+    return (i < a_t ? i : i + skip) * kQ1Tile;
+  };
+  auto tile_ok = [&](int k) { return (k * p.splits + rank) * kQ1Warps + w < n_tiles; };
+  const int lead = kPair ? w & ~1 : w;                        // both warps of a pair make the same rounds
+  const int per = p.splits * kQ1Warps, at0 = rank * kQ1Warps + lead;
+  const int rounds = n_tiles > at0 ? (n_tiles - at0 + per - 1) / per : 0;
+  auto tile_page = [&](int k) -> int32_t { return k < rounds && tile_ok(k) ? __ldg(table + (tile_pos(k) >> 8)) : -1; };
+  bool timed_out = false;
+  int issued = 0;   // tiles whose copies this warp has started (its first `issued` rounds)
+  auto issue_tile = [&](int k, int32_t page) {
+    if (k >= rounds || timed_out) return;
+    issued = k + 1;
+    if (lane == 0 && tile_ok(k) && !(p.test_withhold && k == 0)) {
+      const int c = tile_pos(k);
+      const int b = w * kQ1Stages + (k % kQ1Stages);
+      const uint32_t bar = base + kWdBarOff + b * 8;
+      if (page < 0 || page >= p.num_pages) {
+        record_error(p.status, TQ4_ERR_PAGE_RANGE);
+        page = 0;   // still completes the barrier; the call's output is then undefined
+      }
+      const int slot0 = h * kPage + (c & (kPage - 1));
+      const int row = page * kRowsPerPage + slot0;
+      const uint8_t* pg = p.pool + int64_t(page) * kPageBytes;
+      const uint32_t dst = buf_addr(b), ndst = base + kWdNrmOff + b * 128;
+      mbar_expect_tx(bar, 2 * kQ1KV + 4 * kQ1Tile);
+      tma_load_2d(dst, &tmap, 0, row, bar);                       // K words of 32 positions
+      tma_load_2d(dst + kQ1KV, &tmap, 0, row + 4 * kPage, bar);   // V words
+      bulk_load(ndst, pg + kKNorms + slot0 * 2, 2 * kQ1Tile, bar);
+      bulk_load(ndst + 64, pg + kVNorms + slot0 * 2, 2 * kQ1Tile, bar);
+    }
+  };
+  issue_tile(0, tile_page(0));
+  int32_t page_next = tile_page(1);
+
+  // ---- q' = R q, brought to [0.5, 1) by a power of two per row (undone with the scale in
+  // the scores), f16 hi and lo, in the k order of the table lookups
+  for (int row = w; row < kRows; row += kQ1Warps) {
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (row < n_rows) {
+      const uint4 raw = __ldg(reinterpret_cast<const uint4*>(
+          p.q + (out_row0 + (row / kGroup) * kHq + row % kGroup) * kD + lane * 8));
+      const uint32_t ww[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = apply_sign(__uint_as_float(ww[i] << 16), sb, 2 * i);
+        v[2 * i + 1] = apply_sign(__uint_as_float(ww[i] & 0xFFFF0000u), sb, 2 * i + 1);
+      }
+      warp_fwht256(v);
+    }
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+    const int e = min(max(int(__float_as_uint(amax) >> 23) - 126, -100), 100);
+    const float down = __uint_as_float(uint32_t(127 - e) << 23);
+    if (lane == 0) row_fac[row] = __uint_as_float(uint32_t(127 + e) << 23) * (p.scale * 0.0625f * kLog2e);
+    const int tt = (lane & 15) >> 2, wsel = (lane & 3) + 4 * (lane >> 4);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const int kk = 2 * wsel + (i >> 2);
+      const int col = kk * 16 + ((i >> 1) & 1) * 8 + 2 * tt;
+      const __half2 hi = __floats2half2_rn(v[i] * down, v[i + 1] * down);
+      *reinterpret_cast<__half2*>(qv_hi + row * kQvStride + col) = hi;
+      if constexpr (kExact) {
+        const float2 hf = __half22float2(hi);
+        *reinterpret_cast<__half2*>(qv_lo + row * kQvStride + col) =
+            __floats2half2_rn(v[i] * down - hf.x, v[i + 1] * down - hf.y);
+      }
+    }
+  }
+  __syncthreads();
+
+  // q' B fragments: in registers for one n-tile, read two k-steps at a time otherwise
+  const int qfrag_off = (lane & 7) * kQvStride + ((lane >> 4) & 1) * 16 + ((lane >> 3) & 1) * 8;
+  const uint32_t qh_addr = smem_u32(qv_hi + qfrag_off), ql_addr = smem_u32(qv_lo + qfrag_off);
+  constexpr uint32_t kQTile = 8 * kQvStride * 2;   // bytes between n-tiles
+  uint32_t qh[kPair ? 1 : 16][2];
+  if constexpr (!kPair) {
+#pragma unroll
+    for (int kk = 0; kk < 16; kk += 2)
+      ldmatrix_x4(qh[kk][0], qh[kk][1], qh[kk + 1][0], qh[kk + 1][1], qh_addr + kk * 32);
+  }
+  float fac[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) fac[n][e] = row_fac[8 * n + 2 * t + e];
+
+  float m_ref[NT][2], l_part[NT][2];
+  float o[kMT][NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m_ref[n][e] = -INFINITY;
+      l_part[n][e] = 0.f;
+    }
+#pragma unroll
+  for (int m = 0; m < kMT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[m][n][i] = 0.f;
+
+  const int pk = q1_sigma(g);                                         // K phase: positions pk, pk + 8
+  const int pv0 = q1_sigma(2 * t), pv1 = q1_sigma(2 * t + 1);         // V phase: pv0, pv1 (+ 8)
+  const uint32_t k_off0 = pk * 128 + ((t ^ (pk & 7)) << 4);
+  const uint32_t k_off1 = pk * 128 + (((4 + t) ^ (pk & 7)) << 4);
+  // V words of this lane: one token: 4g .. 4g + 3 (dims 32 g ..); pair: 16 a + 2g, + 1
+  // (dims 128 a + 16 g ..), conflict-free in both cases under the swizzle
+  const int half_a = w & 1;
+  const int vch = kPair ? 4 * half_a + (g >> 1) : g;
+  const uint32_t vsub = kPair ? 8u * uint32_t(g & 1) : 0u;
+  const uint32_t v_off0 = pv0 * 128 + ((vch ^ (pv0 & 7)) << 4) + vsub;
+  const uint32_t v_off1 = pv1 * 128 + ((vch ^ (pv1 & 7)) << 4) + vsub;
+
+  for (int k = 0; k < rounds; ++k) {
+    if constexpr (!kPair) {
+      issue_tile(k + 1, page_next);
+      page_next = tile_page(k + 2);
+    }
+    const int b = w * kQ1Stages + (k % kQ1Stages);
+    bool have = tile_ok(k);
+    auto wait_tile = [&](int buf) {
+      const uint32_t bar = base + kWdBarOff + buf * 8;
+      uint32_t spins = 0;
+      bool late = timed_out;
+      while (!late && !mbar_try_wait(bar, (k / kQ1Stages) & 1)) late = ++spins > p.spin_limit;
+      if (__any_sync(0xffffffffu, late)) {
+        if (lane == 0 && !timed_out) record_error(p.status, TQ4_ERR_TIMEOUT);
+        timed_out = true;
+      }
+      return !timed_out;
+    };
+    if (have) have = wait_tile(b);   // warp-uniform; a pair keeps its rounds either way
+    if (!kPair && !have) break;
+    const uint32_t kst = buf_addr(b);
+    const uint32_t nb = base + kWdNrmOff + b * 128;
+    const int c = tile_pos(k);
+
+    // ------------------------------------------------------------ scores of 32 positions
+    float s[2][NT][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[j][n][i] = 0.f;
+    if (have) {
+      uint4 ka[2], kb4[2], kc[2], kd[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t mrow = kst + j * 16 * 128;
+        ka[j] = ld_shared_v4(mrow + k_off0);
+        kb4[j] = ld_shared_v4(mrow + k_off1);
+        kc[j] = ld_shared_v4(mrow + 8 * 128 + k_off0);
+        kd[j] = ld_shared_v4(mrow + 8 * 128 + k_off1);
+      }
+      uint32_t qb[NT][4], ql[NT][4];
+#pragma unroll
+      for (int kk = 0; kk < 16; ++kk) {
+        if ((kk & 1) == 0) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if constexpr (kPair) ldmatrix_x4(qb[n][0], qb[n][1], qb[n][2], qb[n][3], qh_addr + n * kQTile + kk * 32);
+            if constexpr (kExact) ldmatrix_x4(ql[n][0], ql[n][1], ql[n][2], ql[n][3], ql_addr + n * kQTile + kk * 32);
+          }
+        }
+        const int x = 2 * (kk & 1);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t wg = pick(ka[j], kb4[j], kk >> 1);
+          const uint32_t wg8 = pick(kc[j], kd[j], kk >> 1);
+          uint32_t a0, a1, a2, a3, r0 = 0, r1 = 0, r2 = 0, r3 = 0;
+          if (kk & 1) {
+            if constexpr (kExact) {
+              lut64k<2>(wg, lanebase, a0, r0); lut64k<2>(wg8, lanebase, a1, r1);
+              lut64k<3>(wg, lanebase, a2, r2); lut64k<3>(wg8, lanebase, a3, r3);
+            } else {
+              a0 = lut64k_hi<2>(wg, lanebase); a1 = lut64k_hi<2>(wg8, lanebase);
+              a2 = lut64k_hi<3>(wg, lanebase); a3 = lut64k_hi<3>(wg8, lanebase);
+            }
+          } else {
+            if constexpr (kExact) {
+              lut64k<0>(wg, lanebase, a0, r0); lut64k<0>(wg8, lanebase, a1, r1);
+              lut64k<1>(wg, lanebase, a2, r2); lut64k<1>(wg8, lanebase, a3, r3);
+            } else {
+              a0 = lut64k_hi<0>(wg, lanebase); a1 = lut64k_hi<0>(wg8, lanebase);
+              a2 = lut64k_hi<1>(wg, lanebase); a3 = lut64k_hi<1>(wg8, lanebase);
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint32_t q0 = kPair ? qb[n][x] : qh[kPair ? 0 : kk][0], q1 = kPair ? qb[n][x + 1] : qh[kPair ? 0 : kk][1];
+            mma_16816(s[j][n], a0, a1, a2, a3, q0, q1);
+            if constexpr (kExact) {
+              mma_16816(s[j][n], a0, a1, a2, a3, ql[n][x], ql[n][x + 1]);
+              mma_16816(s[j][n], r0, r1, r2, r3, q0, q1);
+            }
+          }
+        }
+      }
+    }
+
+    // ------------------------------------------------------------ masks, running maxima
+    float vn[2][2];
+    {
+      const bool full = have && c + kQ1Tile - 1 <= first && (c + kQ1Tile <= p.n_sink || c > T - 1 - p.window);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int at = 16 * j + pk + 8 * x;
+          const float kn = have ? __half2float(__ushort_as_half(ld_shared_u16(nb + 2 * at))) : 0.f;
+          vn[j][x] = have ? __half2float(__ushort_as_half(ld_shared_u16(nb + 64 + 2 * at))) * wd_pscale<kExact>() : 0.f;
+          const int pos = c + at;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float v = s[j][n][2 * x + e] * kn * fac[n][e];
+              if (!full) {
+                const int P = first + (8 * n + 2 * t + e) / kGroup;   // this row's position (past T - 1: a padding row)
+                const bool ok = have && pos < T && pos <= P && (pos > P - p.window || pos < p.n_sink);
+                v = ok ? v : -INFINITY;
+              }
+              s[j][n][2 * x + e] = v;
+            }
+        }
+    }
+    float lmax[NT][2];
+    bool need = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        lmax[n][e] = fmaxf(fmaxf(s[0][n][e], s[0][n][e + 2]), fmaxf(s[1][n][e], s[1][n][e + 2]));
+        need |= lmax[n][e] > m_ref[n][e] + wd_lazy<kExact>();
+      }
+    bool raise = __any_sync(0xffffffffu, need);
+    if constexpr (kPair) {   // rows' maxima of both tiles
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float v = lmax[n][e];
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          lmax[n][e] = v;
+          if (g == 0) mx_s[w * 24 + 8 * n + 2 * t + e] = v;
+        }
+      pair_sync(w >> 1);   // and: the partner has finished the previous round's V words
+      issue_tile(k + 1, page_next);
+      page_next = tile_page(k + 2);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          lmax[n][e] = fmaxf(lmax[n][e], mx_s[(w ^ 1) * 24 + 8 * n + 2 * t + e]);
+          raise |= lmax[n][e] > m_ref[n][e] + wd_lazy<kExact>();
+        }
+      raise = __any_sync(0xffffffffu, raise);
+    }
+    if (raise) {
+      float alpha[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float v = lmax[n][e];
+          if constexpr (!kPair) {
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          }
+          alpha[n][e] = 1.f;
+          if (v > m_ref[n][e] + wd_lazy<kExact>()) {
+            alpha[n][e] = fast_exp2(m_ref[n][e] - v);   // 0 on the first raise
+            m_ref[n][e] = v;
+          }
+          l_part[n][e] *= alpha[n][e];
+        }
+#pragma unroll
+      for (int m = 0; m < kMT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          o[m][n][0] *= alpha[n][0];
+          o[m][n][1] *= alpha[n][1];
+          o[m][n][2] *= alpha[n][0];
+          o[m][n][3] *= alpha[n][1];
+        }
+    }
+
+    // ------------------------------------------------------------ weights -> B fragments
+    uint32_t bh[2][NT][2], bl[2][NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float mu0 = m_ref[n][0] == -INFINITY ? 0.f : m_ref[n][0];
+      const float mu1 = m_ref[n][1] == -INFINITY ? 0.f : m_ref[n][1];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float pw[4], wv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          pw[i] = fast_exp2(s[j][n][i] - ((i & 1) ? mu1 : mu0));
+          // a masked position's norm may be anything: its weight is set, not multiplied
+          wv[i] = s[j][n][i] == -INFINITY ? 0.f : pw[i] * vn[j][i >> 1];
+        }
+        l_part[n][0] += pw[0] + pw[2];
+        l_part[n][1] += pw[1] + pw[3];
+        const __half2 h01 = __floats2half2_rn(wv[0], wv[1]), h23 = __floats2half2_rn(wv[2], wv[3]);
+        bh[j][n][0] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h01));
+        bh[j][n][1] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h23));
+        if constexpr (kExact) {
+          const float2 f01 = __half22float2(h01), f23 = __half22float2(h23);
+          const __half2 l01 = __floats2half2_rn(wv[0] - f01.x, wv[1] - f01.y);
+          const __half2 l23 = __floats2half2_rn(wv[2] - f23.x, wv[3] - f23.y);
+          bl[j][n][0] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&l01));
+          bl[j][n][1] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&l23));
+        }
+      }
+    }
+
+    // ------------------------------------------------------------ O'^T += C_v^T P'^T
+    auto v_phase = [&](uint32_t vst, const uint32_t (&ph)[2][NT][2], const uint32_t (&pl)[2][NT][2]) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t vrow = vst + j * 16 * 128;
+        uint32_t x0[4], x1[4], y0[4], y1[4];
+        if constexpr (kPair) {
+          const uint2 a = ld_shared_v2u(vrow + v_off0), bb = ld_shared_v2u(vrow + v_off1);
+          const uint2 cc = ld_shared_v2u(vrow + 8 * 128 + v_off0), d = ld_shared_v2u(vrow + 8 * 128 + v_off1);
+          x0[0] = a.x; x0[1] = a.y; x1[0] = bb.x; x1[1] = bb.y;
+          y0[0] = cc.x; y0[1] = cc.y; y1[0] = d.x; y1[1] = d.y;
+        } else {
+          const uint4 a = ld_shared_v4(vrow + v_off0), bb = ld_shared_v4(vrow + v_off1);
+          const uint4 cc = ld_shared_v4(vrow + 8 * 128 + v_off0), d = ld_shared_v4(vrow + 8 * 128 + v_off1);
+          x0[0] = a.x; x0[1] = a.y; x0[2] = a.z; x0[3] = a.w;
+          x1[0] = bb.x; x1[1] = bb.y; x1[2] = bb.z; x1[3] = bb.w;
+          y0[0] = cc.x; y0[1] = cc.y; y0[2] = cc.z; y0[3] = cc.w;
+          y1[0] = d.x; y1[1] = d.y; y1[2] = d.z; y1[3] = d.w;
+        }
+#pragma unroll
+        for (int q = 0; q < kMT / 4; ++q) {
+          uint32_t lo01, hi01, lo89, hi89;
+          interleave_nibbles(x0[q], x1[q], lo01, hi01);
+          interleave_nibbles(y0[q], y1[q], lo89, hi89);
+#pragma unroll
+          for (int kb = 0; kb < 4; ++kb) {
+            uint32_t a0, a1, a2, a3, r0 = 0, r1 = 0, r2 = 0, r3 = 0;
+            switch (kb) {
+              case 0: lut4<0, kExact>(lo01, hi01, lo89, hi89, lanebase, a0, a1, a2, a3, r0, r1, r2, r3); break;
+              case 1: lut4<1, kExact>(lo01, hi01, lo89, hi89, lanebase, a0, a1, a2, a3, r0, r1, r2, r3); break;
+              case 2: lut4<2, kExact>(lo01, hi01, lo89, hi89, lanebase, a0, a1, a2, a3, r0, r1, r2, r3); break;
+              default: lut4<3, kExact>(lo01, hi01, lo89, hi89, lanebase, a0, a1, a2, a3, r0, r1, r2, r3); break;
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma_16816(o[4 * q + kb][n], a0, a1, a2, a3, ph[j][n][0], ph[j][n][1]);
+              if constexpr (kExact) {
+                mma_16816(o[4 * q + kb][n], a0, a1, a2, a3, pl[j][n][0], pl[j][n][1]);
+                mma_16816(o[4 * q + kb][n], r0, r1, r2, r3, ph[j][n][0], ph[j][n][1]);
+              }
+            }
+          }
+        }
+      }
+    };
+    if constexpr (!kPair) {
+      v_phase(kst + kQ1KV, bh, bl);
+      __syncwarp();   // all lanes are done with this buffer before lane 0 refills it
+    } else {
+      // the weights replace this warp's K words (finished above) for the partner to read
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t at = kst + ((j * NT + n) * 2 + x) * 128 + lane * 4;
+            st_shared_u32(at, bh[j][n][x]);
+            if constexpr (kExact) st_shared_u32(at + 4 * NT * 128, bl[j][n][x]);
+          }
+      // order these stores before the copy that refills the buffer two rounds on
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      pair_sync(w >> 1);
+      const int bp = (w ^ 1) * kQ1Stages + (k % kQ1Stages);
+      const bool have_p = (k * p.splits + rank) * kQ1Warps + (w ^ 1) < n_tiles && wait_tile(bp);
+      if (have) v_phase(kst + kQ1KV, bh, bl);
+      if (have_p) {
+        const uint32_t pst = buf_addr(bp);
+        uint32_t ph[2][NT][2], pl[2][NT][2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t at = pst + ((j * NT + n) * 2 + x) * 128 + lane * 4;
+              ph[j][n][x] = ld_shared_u32(at);
+              pl[j][n][x] = kExact ? ld_shared_u32(at + 4 * NT * 128) : 0u;
+            }
+        v_phase(pst + kQ1KV, ph, pl);
+      }
+      __syncwarp();
+    }
+  }
+  // drain: copies that a warp which gave up may still have in flight
+  if (timed_out) {
+    for (int k = max(issued - kQ1Stages, 0); k < issued; ++k) {
+      if (!tile_ok(k) || (p.test_withhold && k == 0)) continue;
+      const uint32_t bar = base + kWdBarOff + (w * kQ1Stages + (k % kQ1Stages)) * 8;
+      uint32_t spins = 0;
+      while (!mbar_try_wait(bar, (k / kQ1Stages) & 1) && ++spins < kQ1DrainPolls) {
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------- merge: warps, then the cluster
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float lv = l_part[n][e];
+      lv += __shfl_xor_sync(0xffffffffu, lv, 4);
+      lv += __shfl_xor_sync(0xffffffffu, lv, 8);
+      lv += __shfl_xor_sync(0xffffffffu, lv, 16);
+      if (kPair) pair_sync(w >> 1);   // the partner has read this warp's maxima of the last round
+      if (g == 0) {
+        mx_s[w * 24 + 8 * n + 2 * t + e] = m_ref[n][e];
+        l_s[w * 24 + 8 * n + 2 * t + e] = lv;
+      }
+    }
+  __syncthreads();
+  float* const slabs = reinterpret_cast<float*>(smem + (hi_buf - base));   // [slab][rows][pitch], over the tile buffers
+  constexpr int kSlab = kRows * kWdPitch;
+  const int unit = kPair ? w >> 1 : w;
+  float up[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float M = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < kQ1Warps; ++x) M = fmaxf(M, mx_s[x * 24 + 8 * n + 2 * t + e]);
+      up[n][e] = M == -INFINITY ? 0.f : fast_exp2(m_ref[n][e] - M);
+    }
+#pragma unroll
+  for (int pass = 0; pass < (kPair ? 2 : 1); ++pass) {   // pairs 0, 1 write; pairs 2, 3 add
+    if (!kPair || (unit >> 1) == pass) {
+      float* slab = slabs + (kPair ? unit & 1 : unit) * kSlab;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int q = 0; q < kMT / 4; ++q) {
+            float* d = slab + (8 * n + 2 * t + e) * kWdPitch + (kPair ? 128 * half_a + 16 * g : 32 * g) + 8 * q;
+            float v[8];
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+              v[2 * kb] = o[4 * q + kb][n][e] * up[n][e];
+              v[2 * kb + 1] = o[4 * q + kb][n][e + 2] * up[n][e];
+            }
+            float4* d4 = reinterpret_cast<float4*>(d);
+            if (pass == 1) {
+              const float4 a = d4[0], bb = d4[1];
+              v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+              v[4] += bb.x; v[5] += bb.y; v[6] += bb.z; v[7] += bb.w;
+            }
+            d4[0] = make_float4(v[0], v[1], v[2], v[3]);
+            d4[1] = make_float4(v[4], v[5], v[6], v[7]);
+          }
+    }
+    __syncthreads();
+  }
+  // one warp per row: sum the slabs; one CTA: store, several: leave the sum for the cluster
+  float row_m[NT], row_l[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int row = w + 8 * n;
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int x = 0; x < kQ1Warps; ++x) M = fmaxf(M, mx_s[x * 24 + row]);
+#pragma unroll
+    for (int x = 0; x < kQ1Warps; ++x)
+      if (M != -INFINITY) L = fmaf(fast_exp2(mx_s[x * 24 + row] - M), l_s[x * 24 + row], L);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float* src = slabs + row * kWdPitch + lane * 8;
+#pragma unroll
+    for (int x = 0; x < wd_slabs<NT>(); ++x) {
+      const float4 a = reinterpret_cast<const float4*>(src + x * kSlab)[0], bb = reinterpret_cast<const float4*>(src + x * kSlab)[1];
+      acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
+      acc[4] += bb.x; acc[5] += bb.y; acc[6] += bb.z; acc[7] += bb.w;
+    }
+    if (p.splits == 1) {
+      if (row < n_rows)
+        wd_store_row(p, out_row0 + (row / kGroup) * kHq + row % kGroup, acc,
+                     L > 0.f ? 0.0625f / (wd_pscale<kExact>() * L) : 0.f, sb);
+    } else {
+      reinterpret_cast<float4*>(src)[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      reinterpret_cast<float4*>(src)[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    }
+    row_m[n] = M;
+    row_l[n] = L;
+  }
+  if (p.splits == 1) return;
+  __syncthreads();   // every warp has read m and l of all warps
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    if (lane == 0) {
+      mx_s[w + 8 * n] = row_m[n];
+      l_s[w + 8 * n] = row_l[n];
+    }
+  wd_cluster_sync();
+  for (int row = rank + p.splits * w; row < n_rows; row += p.splits * kQ1Warps) {
+    float M = -INFINITY, L = 0.f;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const uint32_t mx_a = smem_u32(mx_s + row), l_a = smem_u32(l_s + row), o_a = hi_buf + uint32_t(row * kWdPitch + lane * 8) * 4u;
+    float mr[kWdMaxCluster];
+#pragma unroll
+    for (int x = 0; x < kWdMaxCluster; ++x) {
+      mr[x] = x < p.splits ? ld_cluster_f32(wd_map_rank(mx_a, x)) : -INFINITY;
+      M = fmaxf(M, mr[x]);
+    }
+    if (M != -INFINITY) {
+#pragma unroll
+      for (int x = 0; x < kWdMaxCluster; ++x)
+        if (x < p.splits) {
+          const float f = fast_exp2(mr[x] - M);
+          L = fmaf(f, ld_cluster_f32(wd_map_rank(l_a, x)), L);
+          const float4 a = ld_cluster_v4(wd_map_rank(o_a, x)), bb = ld_cluster_v4(wd_map_rank(o_a + 16, x));
+          acc[0] = fmaf(f, a.x, acc[0]); acc[1] = fmaf(f, a.y, acc[1]);
+          acc[2] = fmaf(f, a.z, acc[2]); acc[3] = fmaf(f, a.w, acc[3]);
+          acc[4] = fmaf(f, bb.x, acc[4]); acc[5] = fmaf(f, bb.y, acc[5]);
+          acc[6] = fmaf(f, bb.z, acc[6]); acc[7] = fmaf(f, bb.w, acc[7]);
+        }
+    }
+    wd_store_row(p, out_row0 + (row / kGroup) * kHq + row % kGroup, acc, L > 0.f ? 0.0625f / (wd_pscale<kExact>() * L) : 0.f, sb);
+  }
+  wd_cluster_sync();   // no CTA leaves while another reads its shared memory
+}
+
+inline cudaError_t window_set_attrs() {
+  cudaError_t e = cudaSuccess;
+  auto set = [&e](const void* k) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kWdDynBytes));
+  };
+  set(reinterpret_cast<const void*>(decode_window_kernel<1, false>));
+  set(reinterpret_cast<const void*>(decode_window_kernel<1, true>));
+  set(reinterpret_cast<const void*>(decode_window_kernel<2, false>));
+  set(reinterpret_cast<const void*>(decode_window_kernel<2, true>));
+  set(reinterpret_cast<const void*>(decode_window_kernel<3, false>));
+  set(reinterpret_cast<const void*>(decode_window_kernel<3, true>));
+  return e;
+}
+
+// CTAs per (request, KV head): the largest power of two up to kWdMaxCluster that keeps the
+// launch within one CTA per SM, but no more than there are rounds of 8 tiles to share out.
+inline int window_splits(int num_sms, int32_t n_req, int32_t n_q, int32_t max_pages, int32_t window, int32_t n_sink) {
+  const int64_t most = std::min<int64_t>(int64_t(max_pages) * kPage, int64_t(window) + n_q - 1 + n_sink + 3 * kQ1Tile);
+  const int64_t tiles = (most + kQ1Tile - 1) / kQ1Tile;
+  int s = 1;
+  while (s < kWdMaxCluster && int64_t(n_req) * kHkv * s * 2 <= num_sms && tiles > s * kQ1Warps) s *= 2;
+  return s;
+}
+
+inline size_t window_workspace_bytes(int, int32_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
+
+inline cudaError_t launch_decode_window(const WindowParams& p, const CUtensorMap& map, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(p.n_req) * unsigned(p.splits), kHkv);
+  cfg.blockDim = dim3(kQ1Threads);
+  cfg.dynamicSmemBytes = kWdDynBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(p.splits);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const bool exact = p.out_dtype == TQ4_DTYPE_F32;
+  switch (decode_nt(p.n_q)) {
+    case 1: return exact ? cudaLaunchKernelEx(&cfg, decode_window_kernel<1, true>, p, map) : cudaLaunchKernelEx(&cfg, decode_window_kernel<1, false>, p, map);
+    case 2: return exact ? cudaLaunchKernelEx(&cfg, decode_window_kernel<2, true>, p, map) : cudaLaunchKernelEx(&cfg, decode_window_kernel<2, false>, p, map);
+    default: return exact ? cudaLaunchKernelEx(&cfg, decode_window_kernel<3, true>, p, map) : cudaLaunchKernelEx(&cfg, decode_window_kernel<3, false>, p, map);
+  }
+}
+
+}  // namespace tq4

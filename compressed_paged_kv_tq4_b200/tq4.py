@@ -53,6 +53,9 @@ EXPORTS = (
     "tq4_ctx_set_decode_path", "tq4_tqb_codebook", "tq4_tqb_encode_append", "tq4_tqb_decode_attention",
     "tq4_tqb_decode_append_attention", "tq4_tqb_prefill_attention", "tq4_tqb_reconstruct",
     "tq4_tqb_decode_attention_shared",
+    # the ragged serving step
+    "tq4_plan_step", "tq4_rope_table", "tq4_rope_append", "tq4_reconstruct_slots",
+    "tq4_decode_window_workspace_bytes", "tq4_decode_attention_window",
     # host page pool (include/tq4_pages.h)
     "tq4_pages_create", "tq4_pages_destroy", "tq4_pages_reservation", "tq4_pages_admit", "tq4_pages_grow",
     "tq4_pages_finish", "tq4_pages_step_boundary", "tq4_pages_table", "tq4_pages_free_count",
@@ -60,6 +63,8 @@ EXPORTS = (
 )
 NOALLOC_SCRATCH_BYTES = 8 << 20
 DEFAULT_WAIT_POLLS = 1 << 24
+PLAN_MAX_REQUESTS = 16384
+ROPE_MAX_AXES = 3
 
 
 def _load():
@@ -118,6 +123,14 @@ _sig = {
     "tq4_prefill_reconstructed_workspace_bytes": ([_i32, _i32], _sz),
     "tq4_prefill_attention_reconstructed": ([_p, _p, _i32, _p, _i32, _i32, _p, _p, _p, _i32, _f, _p, ctypes.c_int,
                                              _p, _sz, _p], ctypes.c_int),
+    "tq4_plan_step": ([_p, _p, _p, _i32, _p, _i32, _i32, _p, _i32, _p, _p, _p, _p, _i32, _p, _p], ctypes.c_int),
+    "tq4_rope_table": ([_p, _p, _i32, _i32, ctypes.c_double, _p], ctypes.c_int),
+    "tq4_rope_append": ([_p, _p, _i32, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, _i32, _p, _i32, _p, ctypes.c_int,
+                         ctypes.c_int, _p, _i32, _i32, _p, _p, _p, _p], ctypes.c_int),
+    "tq4_reconstruct_slots": ([_p, _p, _i32, _p, _i32, _p, _p, ctypes.c_int, _p], ctypes.c_int),
+    "tq4_decode_window_workspace_bytes": ([_p, _i32, _i32, _i32, _i32, _i32], _sz),
+    "tq4_decode_attention_window": ([_p, _p, _i32, _p, _p, _i32, _p, _i32, _i32, _i32, _i32, _f, _p, ctypes.c_int,
+                                     _p, _sz, _p], ctypes.c_int),
     "tq4_pages_create": ([_i32, ctypes.POINTER(_p)], ctypes.c_int),
     "tq4_pages_destroy": ([_p], ctypes.c_int),
     "tq4_pages_reservation": ([_i64, _i64], _i64),
@@ -335,6 +348,42 @@ def tq4_tqb_prefill_attention(ctx, bits, pool, num_pages, page_table, table_len,
                                           _ptr(workspace), workspace_bytes, _stream(stream))
 
 
+def tq4_plan_step(ctx, past_lens, new_lens, n_req, free_pages, n_free, num_pages, page_tables, max_pages, cu_tok,
+                  seq_lens, tok_pos, tok_slot, max_tok, taken, stream=None) -> int:
+    return _lib.tq4_plan_step(ctx, _ptr(past_lens), _ptr(new_lens), n_req, _ptr(free_pages), n_free, num_pages,
+                              _ptr(page_tables), max_pages, _ptr(cu_tok), _ptr(seq_lens), _ptr(tok_pos),
+                              _ptr(tok_slot), max_tok, _ptr(taken), _stream(stream))
+
+
+def tq4_rope_table(ctx, table, table_len, rot, base, stream=None) -> int:
+    return _lib.tq4_rope_table(ctx, _ptr(table), table_len, rot, base, _stream(stream))
+
+
+def tq4_rope_append(ctx, pool, num_pages, q, k, v, dtype, q_stride, k_stride, v_stride, n_tok, pos, n_axes, sections,
+                    interleaved, adjacent_pairs, table, table_len, rot, slots, q_out, k_out, stream=None) -> int:
+    sec = (_i32 * len(sections))(*sections)
+    return _lib.tq4_rope_append(ctx, _ptr(pool), num_pages, _ptr(q), _ptr(k), _ptr(v), dtype, q_stride, k_stride,
+                                v_stride, n_tok, _ptr(pos), n_axes, ctypes.cast(sec, _p), int(interleaved),
+                                int(adjacent_pairs), _ptr(table), table_len, rot, _ptr(slots), _ptr(q_out),
+                                _ptr(k_out), _stream(stream))
+
+
+def tq4_reconstruct_slots(ctx, pool, num_pages, slots, n, k_out, v_out, out_dtype, stream=None) -> int:
+    return _lib.tq4_reconstruct_slots(ctx, _ptr(pool), num_pages, _ptr(slots), n, _ptr(k_out), _ptr(v_out), out_dtype,
+                                      _stream(stream))
+
+
+def tq4_decode_window_workspace_bytes(ctx, n_req, n_q, max_pages, window, n_sink) -> int:
+    return _lib.tq4_decode_window_workspace_bytes(ctx, n_req, n_q, max_pages, window, n_sink)
+
+
+def tq4_decode_attention_window(ctx, pool, num_pages, q, page_tables, max_pages, seq_lens, n_req, n_q, window, n_sink,
+                                scale, out, out_dtype, workspace, workspace_bytes, stream=None) -> int:
+    return _lib.tq4_decode_attention_window(ctx, _ptr(pool), num_pages, _ptr(q), _ptr(page_tables), max_pages,
+                                            _ptr(seq_lens), n_req, n_q, window, n_sink, scale, _ptr(out), out_dtype,
+                                            _ptr(workspace), workspace_bytes, _stream(stream))
+
+
 def tq4_ctx_set_wait_limit(ctx, polls, withhold_signal=0) -> int:
     return _lib.tq4_ctx_set_wait_limit(ctx, polls, withhold_signal)
 
@@ -465,11 +514,30 @@ def _need_cuda(*ts):
             raise ValueError("TQ4 kernels take CUDA tensors")
 
 
+def _need(name, t, dtype, shape, device, rows=False):
+    """A CUDA tensor of this dtype (or one of several), shape (None: any length) and device;
+    contiguous, or with rows=True of contiguous rows any distance apart."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{name} has dtype {t.dtype}")
+    if t.dim() != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if not (t[:1].is_contiguous() if rows else t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous")
+
+
+_OUT_CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
 class Context:
     """Owns a tq4_ctx for the current device."""
 
     def __init__(self, signs):
         self.handle = tq4_ctx_create(signs)
+        self.device = torch.device("cuda", torch.cuda.current_device())
 
     def close(self):
         if self.handle:
@@ -761,4 +829,115 @@ class Context:
         _check(tq4_tqb_prefill_attention(self.handle, bits, pool, num_pages, page_table, tlen, prefix_len, q, k_chunk,
                                          v_chunk, n_tok, scale, out, od, workspace, workspace.numel(), stream),
                "tq4_tqb_prefill_attention")
+        return out
+
+    # -- the ragged serving step
+    def plan_step(self, past_lens, new_lens, free_pages, page_tables, num_pages, max_tok=None, cu_tok=None,
+                  seq_lens=None, tok_pos=None, tok_slot=None, taken=None, stream=None):
+        """Page tables, token positions and slots of one step from the requests' lengths (all
+        int32 on the device, tok_slot int64). page_tables is updated in place. Give max_tok, or
+        tok_pos and tok_slot of that length. Returns (cu_tok, seq_lens, tok_pos, tok_slot, taken)."""
+        dev, n = self.device, past_lens.numel()
+        if max_tok is None:
+            if tok_pos is None:
+                raise ValueError("give max_tok or tok_pos")
+            max_tok = tok_pos.numel()
+        new = lambda size, dtype: torch.empty(size, dtype=dtype, device=dev)  # noqa: E731
+        cu_tok = new(n + 1, torch.int32) if cu_tok is None else cu_tok
+        seq_lens = new(n, torch.int32) if seq_lens is None else seq_lens
+        tok_pos = new(max_tok, torch.int32) if tok_pos is None else tok_pos
+        tok_slot = new(max_tok, torch.int64) if tok_slot is None else tok_slot
+        taken = new(1, torch.int32) if taken is None else taken
+        for name, t, dtype, shape in (("past_lens", past_lens, torch.int32, (n,)), ("new_lens", new_lens, torch.int32, (n,)),
+                                      ("free_pages", free_pages, torch.int32, (None,)),
+                                      ("page_tables", page_tables, torch.int32, (n, None)),
+                                      ("cu_tok", cu_tok, torch.int32, (n + 1,)), ("seq_lens", seq_lens, torch.int32, (n,)),
+                                      ("tok_pos", tok_pos, torch.int32, (max_tok,)),
+                                      ("tok_slot", tok_slot, torch.int64, (max_tok,)), ("taken", taken, torch.int32, (1,))):
+            _need(name, t, dtype, shape, dev)
+        _check(tq4_plan_step(self.handle, past_lens, new_lens, n, free_pages, free_pages.numel(), num_pages, page_tables,
+                             page_tables.shape[1], cu_tok, seq_lens, tok_pos, tok_slot, max_tok, taken, stream),
+               "tq4_plan_step")
+        return cu_tok, seq_lens, tok_pos, tok_slot, taken
+
+    def rope_table(self, table_len, rot, base, stream=None) -> torch.Tensor:
+        """{cos, sin} of pos * base^(-2 i / rot): float32 [table_len, rot / 2, 2]."""
+        table = torch.empty((table_len, rot // 2, 2), dtype=torch.float32, device=self.device)
+        _check(tq4_rope_table(self.handle, table, table_len, rot, base, stream), "tq4_rope_table")
+        return table
+
+    def rope_append(self, pool, q, k, v, pos, table, slots, sections=None, interleaved=False, pairs="halves",
+                    q_out=None, k_out=None, stream=None):
+        """Rotary positions on q [n, 24, 256] (or None) and k [n, 4, 256], then encode + append of k and
+        v by slot. pos int32 [axes, n] or [n]; table float32 [len, rot / 2, 2]; sections: frequencies per
+        axis; pairs "halves" or "adjacent". Returns q_out (bf16); k_out (bf16), if given, gets the turned keys."""
+        if pairs not in ("halves", "adjacent"):
+            raise ValueError("pairs must be 'halves' or 'adjacent'")
+        dev, n, both = self.device, k.shape[0], (torch.float32, torch.bfloat16)
+        if pos.dim() == 1:
+            pos = pos[None]
+        _need("pool", pool, torch.uint8, (None,), dev)
+        _need("k", k, both, (n, KV_HEADS, HEAD_DIM), dev, rows=True)
+        _need("v", v, k.dtype, (n, KV_HEADS, HEAD_DIM), dev, rows=True)
+        _need("pos", pos, torch.int32, (None, n), dev)
+        _need("table", table, torch.float32, (None, None, 2), dev)
+        _need("slots", slots, torch.int64, (n,), dev)
+        if q is not None:
+            _need("q", q, k.dtype, (n, Q_HEADS, HEAD_DIM), dev, rows=True)
+            if q_out is None:
+                q_out = torch.empty((n, Q_HEADS, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+            _need("q_out", q_out, torch.bfloat16, (n, Q_HEADS, HEAD_DIM), dev)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        if k_out is not None:
+            _need("k_out", k_out, torch.bfloat16, (n, KV_HEADS, HEAD_DIM), dev)
+        rot = 2 * table.shape[1]
+        if sections is None:
+            if pos.shape[0] != 1:
+                raise ValueError("several axes need sections")
+            sections = [rot // 2]
+        if len(sections) != pos.shape[0]:
+            raise ValueError("one section per axis of pos")
+        step = lambda t, heads: heads * HEAD_DIM if t is None or n < 2 else t.stride(0)  # noqa: E731
+        _check(tq4_rope_append(self.handle, pool, pool.numel() // PAGE_BYTES, q, k, v, _OUT_CODES[k.dtype],
+                               step(q, Q_HEADS), step(k, KV_HEADS), step(v, KV_HEADS), n, pos, pos.shape[0],
+                               [int(x) for x in sections], interleaved, pairs == "adjacent", table, table.shape[0], rot,
+                               slots, q_out, k_out, stream), "tq4_rope_append")
+        return q_out
+
+    def reconstruct_slots(self, pool, slots, out_dtype=torch.float32, stream=None):
+        """The stored K and V vectors of int64 slots [n]: two tensors [n, 4, 256] (zeros for negative slots)."""
+        if out_dtype not in _OUT_CODES:
+            raise ValueError("out_dtype must be float32 or bfloat16")
+        _need("pool", pool, torch.uint8, (None,), self.device)
+        _need("slots", slots, torch.int64, (None,), self.device)
+        k = torch.empty((slots.numel(), KV_HEADS, HEAD_DIM), dtype=out_dtype, device=pool.device)
+        v = torch.empty_like(k)
+        _check(tq4_reconstruct_slots(self.handle, pool, pool.numel() // PAGE_BYTES, slots, slots.numel(), k, v,
+                                     _OUT_CODES[out_dtype], stream), "tq4_reconstruct_slots")
+        return k, v
+
+    def decode_window_workspace(self, n_req, n_q, max_pages, window, sinks, device="cuda") -> torch.Tensor:
+        nbytes = tq4_decode_window_workspace_bytes(self.handle, n_req, n_q, max_pages, window, sinks)
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+    def decode_attention_window(self, pool, q, page_tables, seq_lens, window, sinks, scale, out=None,
+                                out_dtype=torch.bfloat16, workspace=None, stream=None):
+        """decode_attention over a sliding window and the first `sinks` positions: q bf16
+        [n_req, n_q, 24, 256], page_tables int32 [n_req, max_pages], seq_lens int32 [n_req] (0: padding, zeros)."""
+        dev, n_req, n_q = self.device, q.shape[0], q.shape[1]
+        _need("pool", pool, torch.uint8, (None,), dev)
+        _need("q", q, torch.bfloat16, (n_req, n_q, Q_HEADS, HEAD_DIM), dev)
+        _need("page_tables", page_tables, torch.int32, (n_req, None), dev)
+        _need("seq_lens", seq_lens, torch.int32, (n_req,), dev)
+        if out is None:
+            out = torch.empty(q.shape, dtype=out_dtype, device=dev)
+        _need("out", out, tuple(_OUT_CODES), tuple(q.shape), dev)
+        max_pages = page_tables.shape[1]
+        if workspace is None and n_req > 0:
+            workspace = self.decode_window_workspace(n_req, n_q, max_pages, window, sinks, dev)
+        _check(tq4_decode_attention_window(self.handle, pool, pool.numel() // PAGE_BYTES, q, page_tables, max_pages,
+                                           seq_lens, n_req, n_q, window, sinks, scale, out, _OUT_CODES[out.dtype],
+                                           workspace, workspace.numel() if workspace is not None else 0, stream),
+               "tq4_decode_attention_window")
         return out

@@ -418,6 +418,107 @@ int tq4_tqb_decode_append_attention(tq4_ctx* ctx, int bits, void* pool, int32_t 
                                     void* out, int out_dtype,
                                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- The ragged serving step: many requests with their own token counts, at once.
+ * The pages admit, grow and page requests ([BUDGET]; simpleprog.com, same page,
+ * section "StateTrans") and run their attention, but give no call for one step of a
+ * batch; these calls are this library's. A step is: tq4_plan_step (lengths -> page
+ * tables, token positions and slots, all on the device), the model's projections,
+ * tq4_rope_append (rotary positions, then encode into the slots), and
+ * tq4_decode_attention_window or tq4_prefill_attention_ragged. No call needs a
+ * length on the host, so a step can be captured in a CUDA graph and replayed.
+ *
+ * A slot is page * 256 + position-in-page; a negative slot is no position. */
+
+/* Page tables, offsets, positions and slots of one step, from the requests' lengths.
+ *   past_lens   device int32 [n_req], positions that are already cached.
+ *   new_lens    device int32 [n_req], new tokens of this step (0: idle).
+ *   free_pages  device int32 [n_free], free page ids, taken from the front.
+ *   page_tables device int32 [n_req][max_pages]: the entries of the cached positions'
+ *               pages are read; entries ceil(past / 256) .. ceil((past + new) / 256) - 1
+ *               are written with fresh pages, request by request; others keep theirs.
+ *   cu_tok      device int32 [n_req + 1] out: first token row of each request.
+ *   seq_lens    device int32 [n_req] out: past + new, or 0 for a refused request.
+ *   tok_pos     device int32 [max_tok] out: position of each token row (0 for padding).
+ *   tok_slot    device int64 [max_tok] out: its slot, -1 for padding rows (behind the
+ *               last request's) and for the rows of a refused request.
+ *   taken       device int32 [1] out: free pages taken.
+ * A request is refused when the free list runs out at it or before it and it needs a
+ * fresh page (TQ4_ERR_NO_PAGES in the status), or when its lengths are negative, pass
+ * its table, or its rows pass max_tok (TQ4_ERR_SEQ); requests that need no page are
+ * served all the same. A refused request keeps its token rows, so cu_tok is the scan of
+ * new_lens (cut at max_tok). A page id outside [0, num_pages) records
+ * TQ4_ERR_PAGE_RANGE and gives slot -1. At most TQ4_PLAN_MAX_REQUESTS requests and
+ * tables of less than 2^31 positions (else TQ4_ERR_UNSUPPORTED). No two of the arrays
+ * may overlap. */
+#define TQ4_PLAN_MAX_REQUESTS 16384
+int tq4_plan_step(tq4_ctx* ctx, const int32_t* past_lens, const int32_t* new_lens, int32_t n_req,
+                  const int32_t* free_pages, int32_t n_free, int32_t num_pages,
+                  int32_t* page_tables, int32_t max_pages, int32_t* cu_tok, int32_t* seq_lens,
+                  int32_t* tok_pos, int64_t* tok_slot, int32_t max_tok, int32_t* taken, void* stream);
+
+/* Table of rotary angles: {cos, sin} of pos * base^(-2 i / rot), formed in 64 bits and
+ * rounded to fp32.
+ *   table  device float [table_len][rot / 2][2], 16-B aligned.
+ * rot: a multiple of 16 up to 256 (else TQ4_ERR_UNSUPPORTED). */
+int tq4_rope_table(tq4_ctx* ctx, float* table, int32_t table_len, int32_t rot, double base, void* stream);
+
+/* Rotary positions on a step's queries and keys, then encode + append of its keys and
+ * values. The first rot dims of each head are turned in pairs:
+ *   y_a = x_a cos - x_b sin,  y_b = x_b cos + x_a sin,
+ * (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) with adjacent_pairs, the angle of pair i
+ * being table[pos[axis(i)]][i]; the other dims pass as they are. q_out (and k_out) hold
+ * the results rounded once to bf16; the cache gets the encode of the unrounded keys and
+ * of the values, as tq4_encode_append's; every quantiser decision and norm is the one
+ * that 64-bit arithmetic takes.
+ *   q, k, v     device, dtype (both fp32 or bf16): token rows of [24][256], [4][256],
+ *               [4][256] elements, q_stride, k_stride, v_stride elements apart (slices of
+ *               one projection are fine); 16-B aligned rows. q and q_out may both be NULL.
+ *   pos         device int32 [n_axes][n_tok], n_axes = 1 .. TQ4_ROPE_MAX_AXES (e.g. time,
+ *               height, width).
+ *   sections    host int32 [n_axes]: frequencies per axis, rot / 2 in all: the first
+ *               sections[0] frequencies to axis 0 and so on; interleaved: frequency i to
+ *               axis i mod n_axes while i < n_axes * sections[axis], the rest to axis 0
+ *               (sections that this does not deal out exactly: TQ4_ERR_ARG).
+ *   table       device, tq4_rope_table's layout; a position outside [0, table_len)
+ *               records TQ4_ERR_SEQ and leaves the token's outputs and slot as they were.
+ *   slots       device int64 [n_tok]: distinct slots; a negative one leaves the token's
+ *               outputs as they were, one past the pool does too and records
+ *               TQ4_ERR_PAGE_RANGE.
+ *   q_out       device bf16 [n_tok][24][256]; may be q itself (bf16, rows 24 * 256 apart).
+ *   k_out       device bf16 [n_tok][4][256] or NULL: the turned keys, for the attention
+ *               of a chunk over its own keys. */
+#define TQ4_ROPE_MAX_AXES 3
+int tq4_rope_append(tq4_ctx* ctx, void* pool, int32_t num_pages, const void* q, const void* k, const void* v,
+                    int dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride, int32_t n_tok,
+                    const int32_t* pos, int32_t n_axes, const int32_t* sections, int interleaved,
+                    int adjacent_pairs, const float* table, int32_t table_len, int32_t rot,
+                    const int64_t* slots, uint16_t* q_out, uint16_t* k_out, void* stream);
+
+/* The stored vectors of a list of slots, as tq4_reconstruct's (export, checks).
+ *   slots        device int64 [n]; a negative slot gives zeros, one past the pool too
+ *                (and TQ4_ERR_PAGE_RANGE).
+ *   k_out, v_out device [n][4][256], out_dtype TQ4_DTYPE_F32, or _BF16 rounded once. */
+int tq4_reconstruct_slots(tq4_ctx* ctx, const void* pool, int32_t num_pages, const int64_t* slots,
+                          int32_t n, void* k_out, void* v_out, int out_dtype, void* stream);
+
+/* Decode attention with a sliding window and sinks: as tq4_decode_attention, but query
+ * token t of a request, at position P = seq_len - n_q + t, sees the positions j <= P
+ * with j > P - window or j < n_sink. Only the pages that hold such positions are read
+ * (entries of others may be anything). One launch. A request of length 0 (refused, or
+ * padding of the batch) gives zeros; a length below n_q or past the table gives zeros and
+ * records TQ4_ERR_SEQ. window >= 1; a window of the whole history is the plain decode.
+ * bf16 results carry the queries, the centroids and the weights as single f16 operands
+ * (each rounded once, relative 2^-11); fp32 results as hi + lo pairs.
+ *   workspace    device, at least tq4_decode_window_workspace_bytes(...) bytes, 256-B
+ *                aligned; NULL where that is 0. */
+size_t tq4_decode_window_workspace_bytes(const tq4_ctx* ctx, int32_t n_req, int32_t n_q,
+                                         int32_t max_pages, int32_t window, int32_t n_sink);
+int tq4_decode_attention_window(tq4_ctx* ctx, const void* pool, int32_t num_pages,
+                                const uint16_t* q, const int32_t* page_tables, int32_t max_pages,
+                                const int32_t* seq_lens, int32_t n_req, int32_t n_q,
+                                int32_t window, int32_t n_sink, float scale, void* out, int out_dtype,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronise the stream, return the first device-side error recorded since
  * the last call (TQ4_OK if none) and clear it. */
 int tq4_get_status(tq4_ctx* ctx, void* stream);

@@ -1,0 +1,305 @@
+"""The ragged serving step's plan, rotary append and slot export on the GPU, against the
+fp64 oracle (oracle/step_oracle.py). Plans and packed words are whole numbers and have to be
+equal; the rotated bf16 outputs are off by half a bf16 step (2^-8 relative) and the fp32
+rotation (a few 2^-24 of the pair)."""
+import numpy as np
+import pytest
+
+from compressed_paged_kv_tq4_b200 import inputs as I
+from oracle import step_oracle as S
+from oracle import tq4_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+from compressed_paged_kv_tq4_b200 import tq4  # noqa: E402
+
+CFG = 41
+
+
+def _i32(a):
+    return torch.from_numpy(np.ascontiguousarray(a, np.int32)).cuda()
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    return tq4.Context(I.signs(CFG))
+
+
+# ---------------------------------------------------------------- plan
+def _plan(ctx, past, new, free, tables, num_pages, max_tok):
+    t = _i32(tables)
+    got = ctx.plan_step(_i32(past), _i32(new), _i32(free), t, num_pages, max_tok=max_tok)
+    torch.cuda.synchronize()
+    return (t, *got)
+
+
+def _check_plan(ctx, past, new, free, tables, num_pages, max_tok):
+    got = [x.cpu().numpy() for x in _plan(ctx, past, new, free, tables, num_pages, max_tok)]
+    exp = S.plan_step(past, new, free, tables, num_pages, max_tok)
+    for name, g, e in zip(("tables", "cu", "lens", "pos", "slot"), got, exp):
+        assert np.array_equal(g, e), name
+    assert got[5][0] == exp[5]
+    status = ctx.status()
+    codes = {"seq": tq4.TQ4_ERR_SEQ, "pages": tq4.TQ4_ERR_NO_PAGES, "page_range": tq4.TQ4_ERR_PAGE_RANGE}
+    assert status in {codes[c] for c in exp[6]} if exp[6] else status == tq4.TQ4_OK
+    return exp
+
+
+@pytest.mark.parametrize("n_req", [1, 2, 31, 33, 1024, 1025, 3000])
+@pytest.mark.parametrize("scarce", [False, True])
+def test_plan_matches_the_oracle(ctx, n_req, scarce):
+    rng = np.random.default_rng(n_req)
+    past = rng.integers(0, 1200, n_req)
+    past[::5] = 256 * rng.integers(0, 4, past[::5].size)   # whole pages
+    new = rng.integers(0, 4, n_req)
+    new[::7] = rng.integers(0, 700, new[::7].size)
+    max_pages = 8
+    tab = np.full((n_req, max_pages), -1)
+    ids = rng.permutation(n_req * max_pages)
+    has = -(-past // 256)
+    at = 0
+    for r in range(n_req):
+        tab[r, :has[r]] = ids[at:at + has[r]]
+        at += has[r]
+    fresh = int((-(-(past + new) // 256) - has).sum())
+    free = ids[at:at + (fresh // 2 if scarce else fresh + 3)]
+    exp = _check_plan(ctx, past, new, free, tab, n_req * max_pages, int(new.sum()) + 13)
+    assert ("pages" in exp[6]) == (scarce and fresh > 1 or (scarce and fresh == 1))
+
+
+def test_plan_edges(ctx):
+    tab = np.full((5, 2), -1)
+    tab[1, 0], tab[3, 0] = 3, 99   # 99: outside the pool
+    # a new request, one token after 255, an idle one, one on a bad page, a full table
+    _check_plan(ctx, [0, 255, 77, 10, 0], [1, 1, 0, 2, 512], [5, 6, 7], tab, 8, 600)
+    # past the table; negative lengths; rows past max_tok
+    _check_plan(ctx, [512, -1, 0, 0], [1, 3, -2, 4], [5, 6], np.full((4, 2), -1), 8, 10)
+    _check_plan(ctx, [0, 0, 0], [300, 300, 1], [0, 1, 2, 3, 4], np.full((3, 2), -1), 8, 301)
+    # no requests, no free pages, no rows
+    _check_plan(ctx, [], [], [1], np.full((0, 2), -1), 4, 3)
+    _check_plan(ctx, [10, 0], [3, 0], [], np.full((2, 1), 1), 4, 3)
+    _check_plan(ctx, [10], [0], [], np.full((1, 1), 1), 4, 0)
+
+
+def test_plan_leaves_other_entries_alone_and_repeats(ctx):
+    tab = np.arange(24).reshape(3, 8)
+    args = ([300, 512, 1], [100, 256, 254], [30, 31, 32], tab, 40, 700)
+    a = _plan(ctx, *args)
+    b = _plan(ctx, *args)
+    assert all(torch.equal(x, y) for x, y in zip(a, b)) and ctx.status() == tq4.TQ4_OK
+    exp = tab.copy()
+    exp[1, 2] = 30
+    assert np.array_equal(a[0].cpu().numpy(), exp)
+
+
+# ---------------------------------------------------------------- rotary append
+def _case(rng, n, dtype, spread=1.0, pad=0):
+    qkv = torch.from_numpy(rng.normal(size=(n, 32 * 256)).astype(np.float32) * spread).to(dtype)
+    pages = -(-n // 256) + 2
+    at = int(rng.integers(0, 256)) + np.arange(n)
+    slot = rng.permutation(pages)[at // 256].astype(np.int64) * 256 + at % 256
+    if pad:
+        slot[rng.permutation(n)[:pad]] = -1
+    return qkv, slot, pages
+
+
+def _views(qkv):
+    n = qkv.shape[0]
+    return qkv[:, :6144].view(n, 24, 256), qkv[:, 6144:7168].view(n, 4, 256), qkv[:, 7168:].view(n, 4, 256)
+
+
+def _table(length, rot, base=1e6):
+    ang = np.arange(length)[:, None] * base ** (-np.arange(rot // 2) / (rot // 2))
+    return np.stack([np.cos(ang), np.sin(ang)], -1).astype(np.float32)
+
+
+def _check_rope(ctx, qkv, slot, pages, pos, table, sections, interleaved, pairs, k_out=True):
+    dev = qkv.cuda()
+    q, k, v = _views(dev)
+    n = qkv.shape[0]
+    before = np.random.default_rng(0).integers(0, 256, pages * 266240, dtype=np.uint8)
+    pool = torch.from_numpy(before).cuda()
+    q_out = torch.full((n, 24, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    kr = torch.full((n, 4, 256), 7.0, dtype=torch.bfloat16, device="cuda") if k_out else None
+    ctx.rope_append(pool, q, k, v, _i32(pos), torch.from_numpy(table).cuda(), torch.from_numpy(slot).cuda(),
+                    sections=sections, interleaved=interleaved, pairs=pairs, q_out=q_out, k_out=kr)
+    torch.cuda.synchronize()
+    assert ctx.status() == tq4.TQ4_OK
+    half = table.shape[1]
+    cs = table.astype(np.float64)[np.asarray(pos)[S.rope_axes(half, sections, interleaved)].T, np.arange(half)]
+    x = [t.cpu().double().numpy() for t in _views(qkv)]
+    turn = lambda a: S.rope_turn(a, cs[..., 0], cs[..., 1], pairs == "adjacent")  # noqa: E731
+    live = slot >= 0
+    for got, src in ((q_out, x[0]), (kr, x[1])):
+        if got is None:
+            continue
+        exp, got = turn(src), got.cpu().double().numpy()
+        # one bf16 rounding after fp32 sums of two products (three roundings, of at most the pair's larger term)
+        err, tol = np.abs(got - exp), 2.0 ** -8 * np.abs(exp) + 2.0 ** -21 * np.abs(src).max() + 2.0 ** -133
+        assert (err <= tol)[live].all()
+        assert (got[~live] == 7.0).all()
+    exp_pool = before.copy()
+    S.store(exp_pool, slot, turn(x[1]), x[2], I.signs(CFG), O.codebook()[0])
+    diff = pool.cpu().numpy() != exp_pool
+    assert not diff.any(), f"{diff.sum()} bytes of the pool differ"
+    # the stored vectors of the slots: fp32 within its own arithmetic, bf16 rounded once
+    ids = torch.from_numpy(slot).cuda()
+    exp = [O.decode_vectors(*self_rows(exp_pool, slot, kv), I.signs(CFG), O.codebook()[0]) for kv in range(2)]
+    for dtype, half_step in ((torch.float32, 2.0 ** -24), (torch.bfloat16, 2.0 ** -8)):
+        hats = ctx.reconstruct_slots(pool, ids, out_dtype=dtype)
+        for hat, e in zip(hats, exp):
+            e = np.where(live[:, None, None], e, 0.0)
+            # eight levels of fp32 sums of 256 terms of at most max |c| norm / 16: 8 * 2^-24 * their 1-norm (<= 16 norms / 16)
+            size = np.linalg.norm(e, axis=-1, keepdims=True)
+            err = np.abs(hat.cpu().double().numpy() - e)
+            assert (err <= half_step * np.abs(e) + 16 * 2.0 ** -24 * size).all()
+    assert ctx.status() == tq4.TQ4_OK
+
+
+def self_rows(pool, slot, kv):
+    words, norms = O._regions(pool)[kv], O._regions(pool)[2 + kv]
+    s = np.maximum(slot, 0)
+    return (np.stack([words[s // 256, h, s % 256] for h in range(4)], 1),
+            np.stack([norms[s // 256, h, s % 256] for h in range(4)], 1))
+
+
+@pytest.mark.parametrize("rot,sections,interleaved,pairs", [
+    (64, [32], False, "halves"), (64, [11, 11, 10], True, "halves"), (64, [12, 10, 10], False, "adjacent"),
+    (16, [8], False, "adjacent"), (16, [4, 4], True, "halves"), (256, [128], False, "halves"),
+    (256, [44, 42, 42], True, "adjacent"), (240, [0, 100, 20], False, "halves"), (112, [56], True, "halves")])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [1, 67])
+def test_rope_append_matches_the_oracle(ctx, rot, sections, interleaved, pairs, dtype, n):
+    rng = np.random.default_rng(rot + n)
+    qkv, slot, pages = _case(rng, n, dtype, pad=n // 5)
+    pos = rng.integers(0, 5000, (len(sections), n))
+    _check_rope(ctx, qkv, slot, pages, pos, _table(5000, rot), sections, interleaved, pairs, k_out=n > 1)
+
+
+def test_rope_append_decisions_over_many_vectors(ctx):
+    """80,000 vectors: about 2,000 of them have a coordinate within 1e-6 of a boundary."""
+    rng = np.random.default_rng(9)
+    qkv, slot, pages = _case(rng, 10_000, torch.float32, spread=3.0)
+    pos = 200_000 + rng.integers(0, 29_000, (1, 10_000))
+    _check_rope(ctx, qkv, slot, pages, pos, _table(229_000, 64), [32], False, "halves")
+
+
+def test_rope_append_of_extreme_vectors(ctx):
+    """Zero, tiny (squares below fp32's range), one-hot, fp16-midpoint and huge vectors."""
+    n = 8
+    qkv = torch.zeros((n, 32 * 256))
+    q, k, v = _views(qkv)
+    k[1], v[1] = 1e-30, -1e-30
+    k[2, :, 100], v[2, :, 3] = 2.0, -2.0
+    k[3, :, 200] = 1.0 + 2.0 ** -11          # an fp16 midpoint: ties to even, 1.0
+    v[3, :, 200] = 1.0 + 3 * 2.0 ** -11      # ties to even, 1 + 2^-9
+    k[4], v[4] = 1e20, 3e38 / 256            # norms past fp16: infinite
+    k[5], v[5] = 4000.0, 4093.99             # norms of 64,000 and 65,503.8 (below the largest fp16)
+    k[6, :, ::2], v[6] = 1e-7, 3e-9          # subnormal fp16 norms
+    pos = np.zeros((1, n), np.int64)
+    with np.errstate(over="ignore"):
+        live = np.arange(n, dtype=np.int64)
+        dev = qkv.cuda()
+        pool = tq4.Context.new_pool(1)
+        qd, kd, vd = _views(dev)
+        ctx.rope_append(pool, qd, kd, vd, _i32(pos), torch.from_numpy(_table(1, 64)).cuda(), torch.from_numpy(live).cuda())
+        torch.cuda.synchronize()
+        exp = O.new_pool(1)
+        S.store(exp, live, k.double().numpy(), v.double().numpy(), I.signs(CFG), O.codebook()[0])
+    kw, vw, kn, vn = O._regions(pool.cpu().numpy())
+    ekw, evw, ekn, evn = O._regions(exp)
+    assert np.array_equal(kn[0, :, :n], ekn[0, :, :n]) and np.array_equal(vn[0, :, :n], evn[0, :, :n])
+    # flat rows make rotated coordinates of exactly 0, where the 64-bit sums' order decides the sign: one-hot
+    # rows (all coordinates 1/16) and the rest compare word by word where the oracle is off the boundary
+    for got, e in ((kw, ekw), (vw, evw)):
+        for row in (0, 2, 3, 7):
+            assert np.array_equal(got[0, :, row], e[0, :, row])
+    assert ctx.status() == tq4.TQ4_OK
+
+
+def test_rope_append_in_place_and_contiguous(ctx):
+    rng = np.random.default_rng(3)
+    n = 5
+    q = torch.from_numpy(rng.normal(size=(n, 24, 256)).astype(np.float32)).bfloat16().cuda()
+    k, v = (torch.from_numpy(rng.normal(size=(n, 4, 256)).astype(np.float32)).bfloat16().cuda() for _ in range(2))
+    pos, table = _i32(rng.integers(0, 100, n)), ctx.rope_table(100, 64, 1e4)
+    slots = torch.arange(n, device="cuda") + 250
+    pools = [tq4.Context.new_pool(2) for _ in range(3)]
+    out = ctx.rope_append(pools[0], q, k, v, pos, table, slots)
+    twin = q.clone()
+    assert ctx.rope_append(pools[1], twin, k, v, pos, table, slots, q_out=twin) is twin
+    assert torch.equal(out, twin) and torch.equal(pools[0], pools[1])
+    assert ctx.rope_append(pools[2], None, k, v, pos, table, slots) is None   # keys and values only
+    assert torch.equal(pools[0], pools[2]) and ctx.status() == tq4.TQ4_OK
+
+
+def test_rope_table(ctx):
+    got = ctx.rope_table(229_376, 64, 1e6).cpu().double().numpy()
+    ang = np.arange(229_376)[:, None] * 1e6 ** (-np.arange(32) / 32)
+    # rounded once from 64 bits; the angle's own 64-bit error is at most 229,376 * 2^-51
+    assert np.abs(got[..., 0] - np.cos(ang)).max() <= 2.0 ** -24 and np.abs(got[..., 1] - np.sin(ang)).max() <= 2.0 ** -24
+
+
+def test_rope_append_bad_positions_and_slots_leave_the_token(ctx):
+    rng = np.random.default_rng(5)
+    n = 4
+    qkv, _, _ = _case(rng, n, torch.float32)
+    q, k, v = _views(qkv.cuda())
+    table = torch.from_numpy(_table(50, 64)).cuda()
+    good = np.arange(n, dtype=np.int64)
+    for pos, slot, code in (([0, 50, 2, 3], good, tq4.TQ4_ERR_SEQ), ([0, -1, 2, 3], good, tq4.TQ4_ERR_SEQ),
+                            ([0, 1, 2, 3], np.array([0, 512, 2, 3]), tq4.TQ4_ERR_PAGE_RANGE)):
+        pool = tq4.Context.new_pool(2)
+        q_out = torch.full((n, 24, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+        ctx.rope_append(pool, q, k, v, _i32(pos), table, torch.from_numpy(slot).cuda(), q_out=q_out)
+        torch.cuda.synchronize()
+        assert ctx.status() == code
+        assert (q_out[1] == 7.0).all() and not (q_out[0] == 7.0).all() and not (q_out[3] == 7.0).all()
+        kw, vw, _, _ = O._regions(pool.cpu().numpy())
+        assert not kw[:, :, 1].any() and not vw[:, :, 1].any() and kw[0, :, 3].any()
+    kh, vh = ctx.reconstruct_slots(pool, torch.tensor([512, -5, 3], device="cuda"))
+    assert ctx.status() == tq4.TQ4_ERR_PAGE_RANGE and not kh[:2].any() and not vh[:2].any() and kh[2].any()
+
+
+def test_refusals(ctx):
+    n = 3
+    pool, table = tq4.Context.new_pool(1), torch.zeros((10, 32, 2), device="cuda")
+    k = torch.zeros((n, 4, 256), device="cuda")
+    q = torch.zeros((n, 24, 256), device="cuda")
+    slots, pos = torch.arange(n, device="cuda"), _i32(np.zeros((1, n)))
+    ok = dict(q=q, k=k, v=k.clone(), pos=pos, table=table, slots=slots)
+    ctx.rope_append(pool, **ok)
+    for bad in (dict(q=q.bfloat16()), dict(v=k[:, :3]), dict(k=k.half(), v=k.half()), dict(slots=slots.int()), dict(pos=pos.long()),
+                dict(table=table.double()), dict(pairs="odd"), dict(pos=_i32(np.zeros((2, n)))), dict(slots=slots.cpu()),
+                dict(k=k.transpose(1, 2).contiguous().transpose(1, 2)), dict(q_out=q)):
+        with pytest.raises(ValueError):
+            ctx.rope_append(pool, **{**ok, **bad})
+    two = _i32(np.zeros((2, n)))
+    four = _i32(np.zeros((4, n)))
+    base = torch.zeros(n * 1024 + 8, device="cuda")
+    for bad, code in ((dict(sections=[31]), tq4.TQ4_ERR_ARG), (dict(pos=two, sections=[33, -1]), tq4.TQ4_ERR_ARG),
+                      (dict(pos=two, sections=[10, 22], interleaved=True), tq4.TQ4_ERR_ARG),
+                      (dict(pos=four, sections=[8] * 4), tq4.TQ4_ERR_UNSUPPORTED),
+                      (dict(table=torch.zeros((10, 12, 2), device="cuda"), sections=[12]), tq4.TQ4_ERR_UNSUPPORTED),
+                      (dict(v=base[1:1 + n * 1024].view(n, 4, 256)), tq4.TQ4_ERR_ARG)):
+        with pytest.raises(tq4.TQ4Error) as e:
+            ctx.rope_append(pool, **{**ok, **bad})
+        assert e.value.code == code
+    empty = torch.zeros((0, 4, 256), device="cuda")
+    ctx.rope_append(pool, None, empty, empty, _i32(np.zeros((1, 0))), table, slots[:0])
+    with pytest.raises(tq4.TQ4Error):
+        ctx.rope_table(10, 24, 1e4)
+    with pytest.raises(tq4.TQ4Error):
+        ctx.rope_table(10, 32, float("nan"))
+    with pytest.raises(ValueError):
+        ctx.plan_step(_i32([1]), _i32([1, 2]), _i32([1]), _i32([[1]]), 4, max_tok=4)
+    with pytest.raises(ValueError):
+        ctx.plan_step(_i32([1]), _i32([1]), _i32([1]), _i32([[1]]), 4)
+    with pytest.raises(tq4.TQ4Error):
+        ctx.plan_step(_i32([1]), _i32([1]), _i32([1]), _i32([[1]]), 0, max_tok=4)
+    torch.cuda.synchronize()
+    assert ctx.status() == tq4.TQ4_OK

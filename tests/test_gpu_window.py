@@ -1,0 +1,236 @@
+"""Decode attention with a sliding window and sinks against the fp64 oracle.
+
+Tolerances. fp32 results carry every operand as an f16 hi + lo pair: the library's fp32 bound
+(1e-4 absolute, for values of size 1). bf16 results: half a bf16 step (2^-8 |o|), and three
+independent f16 roundings (the scores' operands, the weights, the centroids), each of at most
+2^-11 relative, of root mean square at most 2^-12 of a value's size v = norm / 16: six of their
+joint standard deviations, 6 sqrt(3) 2^-12 v, bound an element, and over a whole result the
+root mean square error stays below the rounding's own 2^-8 / sqrt(12) plus sqrt(3) 2^-12,
+together 2^-9 of the root mean square value with room of a fifth."""
+import numpy as np
+import pytest
+
+from compressed_paged_kv_tq4_b200 import inputs as I
+from oracle import step_oracle as S
+from oracle import tq4_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+from compressed_paged_kv_tq4_b200 import tq4  # noqa: E402
+
+SCALE = 1.0 / 16.0
+CFG = 42
+BIG = 1 << 30
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    return tq4.Context(I.signs(CFG))
+
+
+def random_pool(rng, pages):
+    """Uniform random codes, norms 16 s with s in [0.5, 2]."""
+    pool = O.new_pool(pages)
+    kw, vw, kn, vn = O._regions(pool)
+    for w in (kw, vw):
+        w[...] = rng.integers(0, 1 << 32, w.shape, dtype=np.uint32)
+    for n in (kn, vn):
+        n[...] = 16.0 * rng.uniform(0.5, 2.0, n.shape)
+    return pool
+
+
+def scattered(rng, lens, spare=2):
+    need = [-(-int(t) // 256) for t in lens]
+    ids = rng.permutation(sum(need) + spare)
+    tab = np.full((len(lens), max(max(need), 1)), -1, np.int32)
+    at = 0
+    for r, n in enumerate(need):
+        tab[r, :n] = ids[at:at + n]
+        at += n
+    return tab, sum(need) + spare
+
+
+def check(got, exp, v_size=2.0):
+    got = got.cpu().double().numpy() if got.dtype == torch.float32 else got.float().cpu().double().numpy()
+    err = np.abs(got - exp)
+    return got, err
+
+
+def assert_close(out, exp, v_size=2.0, scale=SCALE):
+    got, err = check(out, exp)
+    assert np.isfinite(got).all()
+    if out.dtype == torch.float32:
+        # the bound is for scores at 1/16. A score is scale * (q k), its error relative to |q| |k| scale, and an
+        # absolute error d of a score is a relative error d of its weight: at 16 times the scale the error is 16 times it
+        assert err.max() <= 1e-4 * max(1.0, abs(scale) / SCALE), err.max()
+    else:
+        assert (err <= 2.0 ** -8 * np.abs(exp) + 6 * 3 ** 0.5 * 2.0 ** -12 * v_size).all(), err.max()
+        rms = lambda a: np.sqrt(np.mean(np.square(a)))  # noqa: E731
+        if exp.any():
+            assert rms(err) <= 1.2 * 2.0 ** -9 * rms(exp)
+
+
+def _run(ctx, lens, n_q, window, sinks, dtype, seed=0, spoil=True, scale=SCALE):
+    rng = np.random.default_rng(seed)
+    tab, pages = scattered(rng, lens)
+    pool = random_pool(rng, pages)
+    q = torch.from_numpy(rng.normal(size=(len(lens), n_q, 24, 256)).astype(np.float32)).bfloat16()
+    exp = S.decode_attention_window(pool, tab, lens, q.double().numpy(), window, sinks, scale, I.signs(CFG), O.codebook()[0])
+    if spoil:   # pages that nobody sees: ids out of range; norms that nobody sees: NaN and infinities
+        kn, vn = O._regions(pool)[2:]
+        for r, T in enumerate(lens):
+            if T == 0:
+                tab[r] = 10 ** 8
+                continue
+            pos = np.arange(tab.shape[1] * 256)
+            see = S.visible(pos[None], np.arange(T - n_q, T)[:, None], window, sinks).any(0)
+            for i, p in enumerate(tab[r]):
+                part = see[256 * i:256 * i + 256]
+                if p >= 0 and not part.any():
+                    tab[r, i] = -77
+                elif p >= 0:
+                    kn[p][:, ~part] = np.nan
+                    vn[p][:, ~part] = np.inf
+    out = torch.full(q.shape, 9.0, dtype=dtype, device="cuda")
+    got = ctx.decode_attention_window(torch.from_numpy(pool).cuda(), q.cuda(), torch.from_numpy(tab).cuda(),
+                                      torch.tensor(list(lens), dtype=torch.int32, device="cuda"), window, sinks, scale, out=out)
+    torch.cuda.synchronize()
+    assert got is out and ctx.status() == tq4.TQ4_OK
+    assert_close(got, exp, scale=scale)
+    for r, T in enumerate(lens):
+        if T == 0:
+            assert not got[r].any()
+    return got
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n_q", [1, 2, 3, 4])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 300), (31, 4), (257, 0), (700, 33), (BIG, 0), (2 ** 31 - 1, 2 ** 31 - 1)])
+def test_ragged_lengths(ctx, dtype, n_q, window, sinks):
+    _run(ctx, [n_q, 0, 5, 255, 256, 257, 1000, 2049], n_q, window, sinks, dtype, seed=n_q + window % 97)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n_req,n_q", [(1, 1), (1, 4), (5, 1), (9, 2), (38, 1), (40, 3)])
+def test_cluster_sizes(ctx, dtype, n_req, n_q):
+    """One request is spread over eight CTAs, forty over one each."""
+    lens = [int(x) for x in np.linspace(max(n_q, 40), 4700, n_req)][::-1]
+    _run(ctx, lens, n_q, 3000, 70, dtype, seed=n_req)
+
+
+def test_other_scales(ctx):
+    for scale in (1.0, -0.05, 0.0, 1e-3):
+        _run(ctx, [700, 90], 2, 500, 3, torch.float32, scale=scale)
+
+
+def test_masked_rows_of_a_later_token_do_not_leak(ctx):
+    """Token 0 must not feel token 3's position, even with an infinite norm there."""
+    rng = np.random.default_rng(8)
+    tab, pages = scattered(rng, [300])
+    pool = random_pool(rng, pages)
+    q = torch.from_numpy(rng.normal(size=(1, 4, 24, 256)).astype(np.float32)).bfloat16()
+    exp = S.decode_attention_window(pool, tab, [300], q.double().numpy(), 100, 2, SCALE, I.signs(CFG), O.codebook()[0])
+    kn, vn = O._regions(pool)[2:]
+    vn[tab[0, 299 // 256], :, 299 % 256] = np.inf
+    kn[tab[0, 299 // 256], :, 299 % 256] = np.nan
+    got = ctx.decode_attention_window(torch.from_numpy(pool).cuda(), q.cuda(), torch.from_numpy(tab).cuda(),
+                                      torch.tensor([300], dtype=torch.int32, device="cuda"), 100, 2, SCALE, out_dtype=torch.float32)
+    assert np.abs(got[0, :3].cpu().double().numpy() - exp[0, :3]).max() <= 1e-4
+    assert not torch.isfinite(got[0, 3]).any()
+
+
+def test_large_norms_and_one_dominant_score(ctx):
+    rng = np.random.default_rng(12)
+    tab, pages = scattered(rng, [900])
+    pool = random_pool(rng, pages)
+    kn, vn = O._regions(pool)[2:]
+    kn[:, :, 7] = 3000.0     # scores far above the rest
+    vn[:, :, 9::16] = 1000.0
+    q = torch.from_numpy(rng.normal(size=(1, 1, 24, 256)).astype(np.float32)).bfloat16()
+    exp = S.decode_attention_window(pool, tab, [900], q.double().numpy(), 800, 4, SCALE, I.signs(CFG), O.codebook()[0])
+    got = ctx.decode_attention_window(torch.from_numpy(pool).cuda(), q.cuda(), torch.from_numpy(tab).cuda(),
+                                      torch.tensor([900], dtype=torch.int32, device="cuda"), 800, 4, SCALE, out_dtype=torch.float32)
+    # scores reach 3000 * 16 / 16 / 16 * ~4 = 750; hi + lo pairs carry them to 2^-21 relative: 4e-4 in the exponent,
+    # as a relative error of weights between values of up to 1000 / 16 = 63
+    assert np.abs(got.cpu().double().numpy() - exp).max() <= 750 * 3 * 2.0 ** -21 * 63 / 4 + 1e-4
+
+
+def test_bad_lengths_give_zeros_and_a_status(ctx):
+    rng = np.random.default_rng(1)
+    tab, pages = scattered(rng, [300, 300])
+    pool = torch.from_numpy(random_pool(rng, pages)).cuda()
+    q = torch.zeros((2, 2, 24, 256), dtype=torch.bfloat16, device="cuda") + 1
+    t = torch.from_numpy(tab).cuda()
+    for bad in (1, -3, 513):
+        lens = torch.tensor([300, bad], dtype=torch.int32, device="cuda")
+        out = ctx.decode_attention_window(pool, q, t, lens, 50, 1, SCALE)
+        torch.cuda.synchronize()
+        assert ctx.status() == tq4.TQ4_ERR_SEQ and not out[1].any() and out[0].any()
+    t[0, 1] = pages
+    ctx.decode_attention_window(pool, q, t, torch.tensor([300, 300], dtype=torch.int32, device="cuda"), 50, 1, SCALE)
+    assert ctx.status() == tq4.TQ4_ERR_PAGE_RANGE
+
+
+def test_captured_and_replayed_with_other_lengths(ctx):
+    rng = np.random.default_rng(2)
+    tab, pages = scattered(rng, [1500, 1500])
+    pool = random_pool(rng, pages)
+    q = torch.from_numpy(rng.normal(size=(2, 1, 24, 256)).astype(np.float32)).bfloat16()
+    dev = [torch.from_numpy(pool).cuda(), q.cuda(), torch.from_numpy(tab).cuda(), torch.tensor([1, 1], dtype=torch.int32, device="cuda")]
+    out = torch.empty((2, 1, 24, 256), dtype=torch.float32, device="cuda")
+    ws = ctx.decode_window_workspace(2, 1, tab.shape[1], 900, 5)
+    call = lambda: ctx.decode_attention_window(*dev, 900, 5, SCALE, out=out, workspace=ws)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for lens in ([1500, 1], [0, 950], [903, 906]):
+        dev[3].copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        exp = S.decode_attention_window(pool, tab, lens, q.double().numpy(), 900, 5, SCALE, I.signs(CFG), O.codebook()[0])
+        assert_close(out, exp)
+    assert ctx.status() == tq4.TQ4_OK
+
+
+def test_repeats_bit_for_bit_on_two_streams(ctx):
+    a = _run(ctx, [3000, 17], 1, 2000, 4, torch.float32, seed=5)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        b = _run(ctx, [3000, 17], 1, 2000, 4, torch.float32, seed=5)
+    assert torch.equal(a, b)
+
+
+def test_wait_that_runs_out_is_reported_and_the_context_recovers(ctx):
+    args = ([1200, 400], 1, 600, 4, torch.float32)
+    for n_q in (1, 3):
+        rng = np.random.default_rng(0)
+        tab, pages = scattered(rng, [1200])
+        pool = torch.from_numpy(random_pool(rng, pages)).cuda()
+        q = torch.ones((1, n_q, 24, 256), dtype=torch.bfloat16, device="cuda")
+        ctx.set_wait_limit(2000, withhold_signal=True)
+        ctx.decode_attention_window(pool, q, torch.from_numpy(tab).cuda(), torch.tensor([1200], dtype=torch.int32, device="cuda"), 600, 4, SCALE)
+        torch.cuda.synchronize()
+        ctx.set_wait_limit(0)
+        assert ctx.status() == tq4.TQ4_ERR_TIMEOUT
+    _run(ctx, *args)
+
+
+def test_refusals(ctx):
+    pool, q = tq4.Context.new_pool(1), torch.zeros((1, 1, 24, 256), dtype=torch.bfloat16, device="cuda")
+    tab, lens = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    for kw, err in ((dict(window=0), tq4.TQ4Error), (dict(sinks=-1), tq4.TQ4Error), (dict(scale=float("inf")), tq4.TQ4Error),
+                    (dict(q=q.float()), ValueError), (dict(seq_lens=lens.long()), ValueError), (dict(page_tables=tab.cpu()), ValueError),
+                    (dict(q=torch.zeros((1, 5, 24, 256), dtype=torch.bfloat16, device="cuda")), tq4.TQ4Error),
+                    (dict(out=torch.zeros((1, 1, 24, 256), dtype=torch.float16, device="cuda")), ValueError),
+                    (dict(q=torch.zeros((1, 1, 256, 24), dtype=torch.bfloat16, device="cuda").transpose(2, 3)), ValueError)):
+        with pytest.raises(err):
+            ctx.decode_attention_window(**{**dict(pool=pool, q=q, page_tables=tab, seq_lens=lens, window=4, sinks=0, scale=SCALE), **kw})
+    none = ctx.decode_attention_window(pool, q[:0], tab[:0], lens[:0], 4, 0, SCALE)
+    assert none.shape == (0, 1, 24, 256) and ctx.status() == tq4.TQ4_OK
