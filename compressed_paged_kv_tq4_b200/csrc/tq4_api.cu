@@ -19,6 +19,7 @@
 #include "tq4_decode_tc.cuh"
 #include "tq4_decode_window.cuh"
 #include "tq4_step.cuh"
+#include "tq4_prefill_ragged.cuh"
 
 struct tq4_ctx {
   int device;
@@ -248,6 +249,21 @@ int pool_tensor_map(const void* pool, int32_t num_pages, CUtensorMap* map) {
   return r == CUDA_SUCCESS ? TQ4_OK : TQ4_ERR_CUDA;
 }
 
+// Tensor map over f16 rows of 256 dims (512 B): boxes of 64 dims by box_rows rows, 128-byte
+// swizzle in shared memory. Rows past the end read as zeros.
+int rows_tensor_map(const void* rows, int64_t n, int box_rows, CUtensorMap* map) {
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return TQ4_ERR_CUDA;
+  const cuuint64_t dims[2] = {256, cuuint64_t(n)};
+  const cuuint64_t strides[1] = {512};
+  const cuuint32_t box[2] = {64, cuuint32_t(box_rows)};
+  const cuuint32_t elem[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(rows), dims, strides, box, elem,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? TQ4_OK : TQ4_ERR_CUDA;
+}
+
 // Shared-prefix groups from the caller's per-request description (host arrays):
 // requests with the same leader (leader[r] == r for a leader) share their first
 // pages[r] pages. Groups of more members than one group item's rows allow are cut
@@ -435,6 +451,7 @@ int tq4_ctx_create(const int8_t* signs, tq4_ctx** out) {
   if (e == cudaSuccess) e = cudaMemcpyToSymbol(tq4::g_boundaries64, ctx->boundaries, sizeof(ctx->boundaries));
   if (e == cudaSuccess) e = tq4::plan_set_attrs();
   if (e == cudaSuccess) e = tq4::window_set_attrs();
+  if (e == cudaSuccess) e = tq4::ragged_set_attrs();
   if (e == cudaSuccess) e = set_decode_tc_attrs<2>();
   if (e == cudaSuccess) e = set_decode_tc_attrs<3>();
   if (e == cudaSuccess) e = cudaGetSymbolAddress(&ctx->noalloc_scratch, g_noalloc_scratch);
@@ -987,6 +1004,77 @@ int tq4_decode_attention_window(tq4_ctx* ctx, const void* pool, int32_t num_page
   p.spin_limit = ctx->wait_polls;
   p.test_withhold = ctx->withhold;
   return cuda_status(tq4::launch_decode_window(p, map, static_cast<cudaStream_t>(stream)));
+}
+
+size_t tq4_prefill_ragged_workspace_bytes(const tq4_ctx* ctx, int32_t n_req, int32_t n_tok, int32_t max_pages,
+                                          int32_t window, int32_t n_sink, int out_dtype) {
+  if (!ctx || n_req <= 0 || n_tok <= 0 || max_pages <= 0 || window < 1 || n_sink < 0) return 0;
+  return tq4::ragged_layout(ctx->num_sms, n_req, n_tok, max_pages, window, n_sink, out_dtype == TQ4_DTYPE_F32).total;
+}
+
+int tq4_prefill_attention_ragged(tq4_ctx* ctx, const void* pool, int32_t num_pages, const uint16_t* q,
+                                 const uint16_t* k_new, const uint16_t* v_new, int32_t n_tok, const int32_t* cu_tok,
+                                 const int32_t* seq_lens, const int32_t* page_tables, int32_t max_pages, int32_t n_req,
+                                 int32_t window, int32_t n_sink, float scale, void* out, int out_dtype,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (!ctx || n_req < 0 || n_tok < 0) return TQ4_ERR_ARG;
+  if (window < 1 || n_sink < 0 || !std::isfinite(scale)) return TQ4_ERR_ARG;
+  if (out_dtype != TQ4_DTYPE_F32 && out_dtype != TQ4_DTYPE_BF16) return TQ4_ERR_ARG;
+  if (n_req == 0 || n_tok == 0) return TQ4_OK;
+  if (!pool || !q || !k_new || !v_new || !cu_tok || !seq_lens || !page_tables || !out || num_pages <= 0 || max_pages <= 0)
+    return TQ4_ERR_ARG;
+  if (!aligned(pool, 16) || !aligned(q, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(out, 16))
+    return TQ4_ERR_ARG;
+  const bool exact = out_dtype == TQ4_DTYPE_F32;
+  const tq4::RgLayout l = tq4::ragged_layout(ctx->num_sms, n_req, n_tok, max_pages, window, n_sink, exact);
+  const int64_t parts = exact ? 2 : 1;
+  const int64_t q_rows = parts * tq4::kHq * n_tok, kv_rows = parts * 2 * tq4::kHkv * l.store_rows;
+  if (n_req > TQ4_RAGGED_MAX_REQUESTS || int64_t(max_pages) * tq4::kPage > INT32_MAX || q_rows > INT32_MAX ||
+      kv_rows > INT32_MAX)
+    return TQ4_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256)) return TQ4_ERR_WORKSPACE;
+  if (int rc = check_device(ctx)) return rc;
+  char* ws = static_cast<char*>(workspace);
+  tq4::RaggedParams p{};
+  p.pool = static_cast<const uint8_t*>(pool);
+  p.num_pages = num_pages;
+  p.tables = page_tables;
+  p.max_pages = max_pages;
+  p.seq_lens = seq_lens;
+  p.cu = cu_tok;
+  p.n_req = n_req;
+  p.n_tok = n_tok;
+  p.window = window;
+  p.n_sink = n_sink;
+  p.q = q;
+  p.k = k_new;
+  p.v = v_new;
+  p.scale = scale;
+  p.out = out;
+  p.out_dtype = out_dtype;
+  p.signs = ctx->signs;
+  p.status = ctx->d_status;
+  p.spin_limit = ctx->wait_polls;
+  p.test_withhold = ctx->withhold;
+  p.max_pairs = std::max(ctx->num_sms / 2, 1);
+  p.head = reinterpret_cast<tq4::RgHead*>(ws + l.head);
+  p.req = reinterpret_cast<tq4::RgReq*>(ws + l.req);
+  p.blk_req = reinterpret_cast<int32_t*>(ws + l.blk_req);
+  p.blk_cum = reinterpret_cast<int64_t*>(ws + l.blk_cum);
+  p.starts = reinterpret_cast<tq4::RgStart*>(ws + l.starts);
+  p.qr = reinterpret_cast<__half*>(ws + l.qr);
+  p.qfac = reinterpret_cast<float*>(ws + l.qfac);
+  p.rows = reinterpret_cast<__half*>(ws + l.rows);
+  p.norms = reinterpret_cast<float*>(ws + l.norms);
+  p.store_rows = l.store_rows;
+  p.po = reinterpret_cast<float*>(ws + l.po);
+  p.pml = reinterpret_cast<float2*>(ws + l.pml);
+  CUtensorMap qmap, kvmap;
+  if (int rc = rows_tensor_map(p.qr, q_rows, tq4::kPfRows, &qmap)) return rc;
+  if (int rc = rows_tensor_map(p.rows, kv_rows, exact ? 32 : 64, &kvmap)) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_status(exact ? tq4::launch_ragged_t<true>(p, qmap, kvmap, l, ctx->num_sms, st)
+                           : tq4::launch_ragged_t<false>(p, qmap, kvmap, l, ctx->num_sms, st));
 }
 
 int tq4_get_status(tq4_ctx* ctx, void* stream) {

@@ -56,6 +56,7 @@ EXPORTS = (
     # the ragged serving step
     "tq4_plan_step", "tq4_rope_table", "tq4_rope_append", "tq4_reconstruct_slots",
     "tq4_decode_window_workspace_bytes", "tq4_decode_attention_window",
+    "tq4_prefill_ragged_workspace_bytes", "tq4_prefill_attention_ragged",
     # host page pool (include/tq4_pages.h)
     "tq4_pages_create", "tq4_pages_destroy", "tq4_pages_reservation", "tq4_pages_admit", "tq4_pages_grow",
     "tq4_pages_finish", "tq4_pages_step_boundary", "tq4_pages_table", "tq4_pages_free_count",
@@ -64,6 +65,7 @@ EXPORTS = (
 NOALLOC_SCRATCH_BYTES = 8 << 20
 DEFAULT_WAIT_POLLS = 1 << 24
 PLAN_MAX_REQUESTS = 16384
+RAGGED_MAX_REQUESTS = 16384
 ROPE_MAX_AXES = 3
 
 
@@ -131,6 +133,9 @@ _sig = {
     "tq4_decode_window_workspace_bytes": ([_p, _i32, _i32, _i32, _i32, _i32], _sz),
     "tq4_decode_attention_window": ([_p, _p, _i32, _p, _p, _i32, _p, _i32, _i32, _i32, _i32, _f, _p, ctypes.c_int,
                                      _p, _sz, _p], ctypes.c_int),
+    "tq4_prefill_ragged_workspace_bytes": ([_p, _i32, _i32, _i32, _i32, _i32, ctypes.c_int], _sz),
+    "tq4_prefill_attention_ragged": ([_p, _p, _i32, _p, _p, _p, _i32, _p, _p, _p, _i32, _i32, _i32, _i32, _f, _p,
+                                      ctypes.c_int, _p, _sz, _p], ctypes.c_int),
     "tq4_pages_create": ([_i32, ctypes.POINTER(_p)], ctypes.c_int),
     "tq4_pages_destroy": ([_p], ctypes.c_int),
     "tq4_pages_reservation": ([_i64, _i64], _i64),
@@ -382,6 +387,19 @@ def tq4_decode_attention_window(ctx, pool, num_pages, q, page_tables, max_pages,
     return _lib.tq4_decode_attention_window(ctx, _ptr(pool), num_pages, _ptr(q), _ptr(page_tables), max_pages,
                                             _ptr(seq_lens), n_req, n_q, window, n_sink, scale, _ptr(out), out_dtype,
                                             _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def tq4_prefill_ragged_workspace_bytes(ctx, n_req, n_tok, max_pages, window, n_sink, out_dtype) -> int:
+    return _lib.tq4_prefill_ragged_workspace_bytes(ctx, n_req, n_tok, max_pages, window, n_sink, out_dtype)
+
+
+def tq4_prefill_attention_ragged(ctx, pool, num_pages, q, k_new, v_new, n_tok, cu_tok, seq_lens, page_tables, max_pages,
+                                 n_req, window, n_sink, scale, out, out_dtype, workspace, workspace_bytes,
+                                 stream=None) -> int:
+    return _lib.tq4_prefill_attention_ragged(ctx, _ptr(pool), num_pages, _ptr(q), _ptr(k_new), _ptr(v_new), n_tok,
+                                             _ptr(cu_tok), _ptr(seq_lens), _ptr(page_tables), max_pages, n_req, window,
+                                             n_sink, scale, _ptr(out), out_dtype, _ptr(workspace), workspace_bytes,
+                                             _stream(stream))
 
 
 def tq4_ctx_set_wait_limit(ctx, polls, withhold_signal=0) -> int:
@@ -940,4 +958,37 @@ class Context:
                                            seq_lens, n_req, n_q, window, sinks, scale, out, _OUT_CODES[out.dtype],
                                            workspace, workspace.numel() if workspace is not None else 0, stream),
                "tq4_decode_attention_window")
+        return out
+
+    def prefill_ragged_workspace(self, n_req, n_tok, max_pages, window, sinks, out_dtype=torch.float32,
+                                 device="cuda") -> torch.Tensor:
+        """Scratch of prefill_attention_ragged; the default out_dtype's serves both."""
+        nbytes = tq4_prefill_ragged_workspace_bytes(self.handle, n_req, n_tok, max_pages, window, sinks,
+                                                    _OUT_CODES[out_dtype])
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+    def prefill_attention_ragged(self, pool, q, k_new, v_new, cu_tok, seq_lens, page_tables, window, sinks, scale,
+                                 out=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
+        """Chunks of several requests over their paged prefixes: q bf16 [rows, 24, 256], k_new, v_new bf16
+        [rows, 4, 256] (request r's rows are cu_tok[r] .. cu_tok[r + 1] - 1), seq_lens int32 [n_req] with the new
+        positions, page_tables int32 [n_req, max_pages]. Rows behind the last request's are left as they were."""
+        dev, rows, n_req = self.device, q.shape[0], seq_lens.numel()
+        _need("pool", pool, torch.uint8, (None,), dev)
+        _need("q", q, torch.bfloat16, (rows, Q_HEADS, HEAD_DIM), dev)
+        _need("k_new", k_new, torch.bfloat16, (rows, KV_HEADS, HEAD_DIM), dev)
+        _need("v_new", v_new, torch.bfloat16, (rows, KV_HEADS, HEAD_DIM), dev)
+        _need("cu_tok", cu_tok, torch.int32, (n_req + 1,), dev)
+        _need("seq_lens", seq_lens, torch.int32, (n_req,), dev)
+        _need("page_tables", page_tables, torch.int32, (n_req, None), dev)
+        if out is None:
+            out = torch.zeros(q.shape, dtype=out_dtype, device=dev)
+        _need("out", out, tuple(_OUT_CODES), tuple(q.shape), dev)
+        max_pages = page_tables.shape[1]
+        if workspace is None and n_req > 0 and rows > 0:
+            workspace = self.prefill_ragged_workspace(n_req, rows, max_pages, window, sinks, out.dtype, dev)
+        _check(tq4_prefill_attention_ragged(self.handle, pool, pool.numel() // PAGE_BYTES, q, k_new, v_new, rows, cu_tok,
+                                            seq_lens, page_tables, max_pages, n_req, window, sinks, scale, out,
+                                            _OUT_CODES[out.dtype], workspace,
+                                            workspace.numel() if workspace is not None else 0, stream),
+               "tq4_prefill_attention_ragged")
         return out

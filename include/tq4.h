@@ -519,6 +519,43 @@ int tq4_decode_attention_window(tq4_ctx* ctx, const void* pool, int32_t num_page
                                 int32_t window, int32_t n_sink, float scale, void* out, int out_dtype,
                                 void* workspace, size_t workspace_bytes, void* stream);
 
+/* Attention of chunks of several requests at once, over their paged prefixes, with a
+ * sliding window and sinks. Request r's new tokens are the rows cu_tok[r] ..
+ * cu_tok[r + 1] - 1 of q, k_new and v_new, at its positions seq_len - n .. seq_len - 1;
+ * the token at position P sees j <= P with j > P - window or j < n_sink: positions
+ * before the chunk from the cache, the chunk's own from k_new and v_new (as
+ * tq4_prefill_attention; whether the chunk has been appended does not matter).
+ *   q            device bf16 [n_tok][24][256]
+ *   k_new, v_new device bf16 [n_tok][4][256]
+ *   cu_tok       device int32 [n_req + 1], non-decreasing, at most n_tok
+ *   seq_lens     device int32 [n_req], positions INCLUDING the new ones
+ *   page_tables  device int32 [n_req][max_pages]; only the entries of pages that some
+ *                token sees and that lie before the chunk are read.
+ *   out          device [n_tok][24][256], out_dtype. Rows before cu_tok[0] and behind the
+ *                last request's are left as they were; those of a request of length 0
+ *                (refused) are zeros.
+ *   workspace    device, tq4_prefill_ragged_workspace_bytes(...) bytes (same arguments and
+ *                out_dtype), 256-B aligned. Calls that may overlap need one each.
+ * A request whose rows or length are inconsistent (cu_tok out of order or past n_tok, a
+ * length below its tokens or past the table) gets zeros where its rows are its own, and
+ * TQ4_ERR_SEQ is recorded. bf16 results carry the operands as single f16 values (each
+ * rounded once, relative 2^-11), fp32 results as hi + lo pairs. A chunk vector with an
+ * infinity or a NaN makes the results of those who see it NaN, of no other. A rotated
+ * value coordinate of 65,504 or more overflows, as its fp16 norm does in the cache. At most
+ * TQ4_RAGGED_MAX_REQUESTS requests. The workspace holds one f16 row (fp32: two) per visible
+ * position, KV head, K and V: 4 KiB (8 KiB) a position, for at most sinks + window + new
+ * positions of each request. */
+#define TQ4_RAGGED_MAX_REQUESTS 16384
+size_t tq4_prefill_ragged_workspace_bytes(const tq4_ctx* ctx, int32_t n_req, int32_t n_tok,
+                                          int32_t max_pages, int32_t window, int32_t n_sink,
+                                          int out_dtype);
+int tq4_prefill_attention_ragged(tq4_ctx* ctx, const void* pool, int32_t num_pages, const uint16_t* q,
+                                 const uint16_t* k_new, const uint16_t* v_new, int32_t n_tok,
+                                 const int32_t* cu_tok, const int32_t* seq_lens,
+                                 const int32_t* page_tables, int32_t max_pages, int32_t n_req,
+                                 int32_t window, int32_t n_sink, float scale, void* out, int out_dtype,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronise the stream, return the first device-side error recorded since
  * the last call (TQ4_OK if none) and clear it. */
 int tq4_get_status(tq4_ctx* ctx, void* stream);

@@ -1,0 +1,284 @@
+"""Attention of chunks of several requests over their paged prefixes, with a sliding window and
+sinks, against the fp64 oracle; and the whole serving step (plan, rotary append, attention) over
+several steps. Tolerances as in test_gpu_window.py."""
+import numpy as np
+import pytest
+
+from compressed_paged_kv_tq4_b200 import inputs as I
+from oracle import step_oracle as S
+from oracle import tq4_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+from compressed_paged_kv_tq4_b200 import tq4  # noqa: E402
+from test_gpu_window import BIG, CFG, SCALE, assert_close, element_tolerance, random_pool, scattered  # noqa: E402
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    return tq4.Context(I.signs(CFG))
+
+
+def _i32(a):
+    return torch.from_numpy(np.ascontiguousarray(a, np.int32)).cuda()
+
+
+def _bf16(rng, shape):
+    return torch.from_numpy(rng.normal(size=shape).astype(np.float32)).bfloat16()
+
+
+def _case(past, new, seed=0, pad=0, lead=0):
+    rng = np.random.default_rng(seed)
+    lens = [p + n for p, n in zip(past, new)]
+    tab, pages = scattered(rng, lens)
+    pool = random_pool(rng, pages)
+    cu = lead + np.concatenate([[0], np.cumsum(new)])
+    rows = int(cu[-1]) + pad
+    return rng, lens, tab, pool, cu, _bf16(rng, (rows, 24, 256)), _bf16(rng, (rows, 4, 256)), _bf16(rng, (rows, 4, 256))
+
+
+def _oracle(pool, tab, lens, cu, q, k, v, window, sinks, scale=SCALE):
+    return S.prefill_attention_ragged(pool, tab, lens, cu, q.double().numpy(), k.double().numpy(), v.double().numpy(), window, sinks,
+                                      scale, I.signs(CFG), O.codebook()[0])
+
+
+def _spoil(pool, tab, lens, new, window, sinks):
+    """Ids out of range where nobody looks (chunk pages too), NaN and infinite norms at unseen positions."""
+    kn, vn = O._regions(pool)[2:]
+    for r, T in enumerate(lens):
+        first = T - new[r]
+        pos = np.arange(tab.shape[1] * 256)
+        see = np.zeros(pos.size, bool)
+        if new[r]:
+            see = S.visible(pos[None], np.arange(first, T)[:, None], window, sinks).any(0) & (pos < first)
+        for i, p in enumerate(tab[r]):
+            part = see[256 * i:256 * i + 256]
+            if p >= 0 and not part.any():
+                tab[r, i] = 10 ** 7
+            elif p >= 0:
+                kn[p][:, ~part] = np.nan
+                vn[p][:, ~part] = np.inf
+
+
+def _run(ctx, past, new, window, sinks, dtype, seed=0, pad=0, lead=0, scale=SCALE):
+    rng, lens, tab, pool, cu, q, k, v = _case(past, new, seed, pad, lead)
+    exp = _oracle(pool, tab, lens, cu, q, k, v, window, sinks, scale)
+    _spoil(pool, tab, lens, new, window, sinks)
+    out = torch.full(q.shape, 9.0, dtype=dtype, device="cuda")
+    got = ctx.prefill_attention_ragged(torch.from_numpy(pool).cuda(), q.cuda(), k.cuda(), v.cuda(), _i32(cu), _i32(lens), _i32(tab),
+                                       window, sinks, scale, out=out)
+    torch.cuda.synchronize()
+    assert got is out and ctx.status() == tq4.TQ4_OK
+    a, b = int(cu[0]), int(cu[-1])
+    assert (got[:a] == 9.0).all() and (got[b:] == 9.0).all()   # rows of nobody stay as they were
+    assert_close(got[a:b], exp[a:b], scale=scale)
+    return got
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_one_token(ctx, dtype):
+    _run(ctx, [0], [1], BIG, 0, dtype)
+    _run(ctx, [300], [1], 100, 2, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 300), (63, 4), (300, 1), (700, 130), (BIG, 0), (2 ** 31 - 1, 2 ** 31 - 1)])
+def test_ragged(ctx, dtype, window, sinks):
+    """Prefixes that end inside pages and tiles, chunks of one to several row blocks, idle requests."""
+    past = [0, 5, 255, 700, 1000, 0, 1300, 64]
+    new = [1, 43, 0, 85, 3, 130, 42, 64]
+    _run(ctx, past, new, window, sinks, dtype, seed=window % 89 + sinks % 7, pad=5, lead=2)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("past,new,window,sinks", [([4000], [17], BIG, 0), ([0], [300], BIG, 0), ([2500, 90], [200, 250], 900, 40),
+                                                   ([6000], [2], 5000, 4)])
+def test_items_shared_by_pairs(ctx, dtype, past, new, window, sinks):
+    _run(ctx, past, new, window, sinks, dtype, seed=3)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_many_requests(ctx, dtype):
+    """More requests than a scan round, most of them idle, and more blocks than pairs."""
+    n = 300
+    rng = np.random.default_rng(1)
+    new = np.where(rng.random(n) < 0.7, 0, rng.integers(1, 6, n))
+    _run(ctx, rng.integers(0, 70, n).tolist(), new.tolist(), 50, 3, dtype, seed=4)
+
+
+def test_other_scales(ctx):
+    for scale in (1.0, -0.05, 0.0, 1e-3):
+        _run(ctx, [200, 3], [50, 20], 150, 3, torch.float32, scale=scale)
+
+
+def test_whole_prefill_equals_the_one_request_call(ctx):
+    rng, lens, tab, pool, cu, q, k, v = _case([777], [100], seed=6)
+    dev = torch.from_numpy(pool).cuda()
+    one = ctx.prefill_attention(dev, _i32(tab[0]), 777, q.cuda(), k.cuda(), v.cuda(), SCALE, out_dtype=torch.float32)
+    got = ctx.prefill_attention_ragged(dev, q.cuda(), k.cuda(), v.cuda(), _i32(cu), _i32(lens), _i32(tab), BIG, 0, SCALE, out_dtype=torch.float32)
+    assert (one - got).abs().max() <= 2e-4   # each within 1e-4 of the oracle
+
+
+def test_chunk_infinities_reach_only_those_who_see_them(ctx):
+    for dtype in (torch.bfloat16, torch.float32):
+        rng, lens, tab, pool, cu, q, k, v = _case([100, 30], [60, 50], seed=7)
+        exp = _oracle(pool, tab, lens, cu, q, k, v, 20, 1)
+        k[40, 1, 5], v[45, 2, 9], k[50, 0, 0] = float("inf"), float("nan"), float("nan")
+        q[70, 3, 8] = float("inf")
+        got = ctx.prefill_attention_ragged(torch.from_numpy(pool).cuda(), q.cuda(), k.cuda(), v.cuda(), _i32(cu), _i32(lens), _i32(tab),
+                                           20, 1, SCALE, out_dtype=dtype)
+        torch.cuda.synchronize()
+        bad = np.zeros((110, 24), bool)
+        bad[40:60, 6:12] = bad[45:60, 12:18] = bad[50:60, 0:6] = True   # a window of 20 from each, within the request
+        bad[70, 3] = True
+        host = got.float().cpu()
+        assert (~torch.isfinite(host)).all(-1).numpy()[bad].all()
+        assert torch.isfinite(host).numpy().all(-1)[~bad].all()
+        tol = 1e-4 if dtype == torch.float32 else element_tolerance(exp[~bad])
+        assert (np.abs(host.double().numpy()[~bad] - exp[~bad]) <= tol).all()
+
+
+def test_scaled_vectors(ctx):
+    """Queries, keys and values far from size 1: the rows' own powers of two carry them."""
+    rng, lens, tab, pool, cu, q, k, v = _case([150], [90], seed=8)
+    q, k, v = q * 2.0 ** -9, k * 2.0 ** 9, v * 2.0 ** 5
+    exp = _oracle(pool, tab, lens, cu, q, k, v, BIG, 0)
+    got = ctx.prefill_attention_ragged(torch.from_numpy(pool).cuda(), q.cuda(), k.cuda(), v.cuda(), _i32(cu), _i32(lens), _i32(tab),
+                                       BIG, 0, SCALE, out_dtype=torch.float32)
+    assert np.abs(got.cpu().double().numpy() - exp).max() <= 1e-4 * 2.0 ** 5   # values 32 times as large
+
+
+def test_refused_requests_and_bad_offsets(ctx):
+    rng, lens, tab, pool, cu, q, k, v = _case([100, 50, 30], [20, 30, 10], seed=9)
+    dev = [torch.from_numpy(pool).cuda(), q.cuda(), k.cuda(), v.cuda()]
+    exp = _oracle(pool, tab, lens, cu, q, k, v, 40, 2)
+
+    def call(cu_, lens_, code):
+        out = torch.full(q.shape, 9.0, dtype=torch.float32, device="cuda")
+        ctx.prefill_attention_ragged(*dev, _i32(cu_), _i32(lens_), _i32(tab), 40, 2, SCALE, out=out)
+        torch.cuda.synchronize()
+        assert ctx.status() == code
+        return out.cpu().double().numpy()
+
+    got = call(cu, [lens[0], 0, lens[2]], tq4.TQ4_OK)              # a refused request: zeros, the rest as before
+    assert not got[20:50].any() and np.abs(got[:20] - exp[:20]).max() <= 1e-4 and np.abs(got[50:] - exp[50:]).max() <= 1e-4
+    for bad in (29, -1, tab.shape[1] * 256 + 1):                   # lengths below the tokens, negative, past the table
+        got = call(cu, [lens[0], bad, lens[2]], tq4.TQ4_ERR_SEQ)
+        assert not got[20:50].any() and np.abs(got[50:] - exp[50:]).max() <= 1e-4
+    for bad in ([0, 20, 10, 60], [0, 20, 50, 61], [-5, 20, 50, 60], [0, 2 ** 31 - 1, 50, 60], [60, 50, 20, 0], [7, -2 ** 31, 2 ** 31 - 1, 9]):
+        call(bad, lens, tq4.TQ4_ERR_SEQ)                           # nothing is touched out of range
+    got = call([60, 60, 60, 60], lens, tq4.TQ4_OK)                 # idle requests only
+    assert (got == 9.0).all()
+    tab[0, 0] = -1
+    out = call(cu, lens, tq4.TQ4_ERR_PAGE_RANGE)
+    assert np.abs(out[20:] - exp[20:]).max() <= 1e-4
+
+
+def test_captured_and_replayed_with_other_lengths(ctx):
+    rng, lens, tab, pool, cu, q, k, v = _case([500, 500], [60, 60], seed=10)
+    dev = [torch.from_numpy(pool).cuda(), q.cuda(), k.cuda(), v.cuda(), _i32(cu), _i32(lens), _i32(tab)]
+    out = torch.zeros(q.shape, dtype=torch.float32, device="cuda")
+    ws = ctx.prefill_ragged_workspace(2, 120, tab.shape[1], 200, 5)
+    call = lambda: ctx.prefill_attention_ragged(*dev, 200, 5, SCALE, out=out, workspace=ws)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for cu2, lens2 in (([0, 1, 120], [3, 560]), ([0, 119, 120], [119, 400]), ([0, 0, 7], [12, 300])):
+        out.fill_(9.0)
+        dev[4].copy_(torch.tensor(cu2, dtype=torch.int32))
+        dev[5].copy_(torch.tensor(lens2, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        exp = _oracle(pool, tab, lens2, cu2, q, k, v, 200, 5)
+        assert_close(out[:cu2[-1]], exp[:cu2[-1]])
+        assert (out[cu2[-1]:] == 9.0).all()
+    assert ctx.status() == tq4.TQ4_OK
+
+
+def test_repeats_bit_for_bit(ctx):
+    a = _run(ctx, [900, 20], [100, 70], 400, 3, torch.bfloat16, seed=11)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        b = _run(ctx, [900, 20], [100, 70], 400, 3, torch.bfloat16, seed=11)
+    assert torch.equal(a, b)
+
+
+def test_wait_that_runs_out_is_reported_and_the_context_recovers(ctx):
+    rng, lens, tab, pool, cu, q, k, v = _case([700], [90], seed=12)
+    dev = [torch.from_numpy(pool).cuda(), q.cuda(), k.cuda(), v.cuda(), _i32(cu), _i32(lens), _i32(tab)]
+    for dtype in (torch.bfloat16, torch.float32):
+        ctx.set_wait_limit(2000, withhold_signal=True)
+        ctx.prefill_attention_ragged(*dev, BIG, 0, SCALE, out_dtype=dtype)
+        torch.cuda.synchronize()
+        ctx.set_wait_limit(0)
+        assert ctx.status() == tq4.TQ4_ERR_TIMEOUT
+        _run(ctx, [700], [90], BIG, 0, dtype, seed=12)
+
+
+def test_refusals(ctx):
+    rng, lens, tab, pool, cu, q, k, v = _case([10], [4], seed=13)
+    ok = dict(pool=torch.from_numpy(pool).cuda(), q=q.cuda(), k_new=k.cuda(), v_new=v.cuda(), cu_tok=_i32(cu), seq_lens=_i32(lens),
+              page_tables=_i32(tab), window=4, sinks=0, scale=SCALE)
+    for bad, err in ((dict(window=0), tq4.TQ4Error), (dict(sinks=-1), tq4.TQ4Error), (dict(scale=float("nan")), tq4.TQ4Error),
+                     (dict(q=q.cuda().float()), ValueError), (dict(k_new=k.cuda()[:3]), ValueError), (dict(cu_tok=_i32([0])), ValueError),
+                     (dict(v_new=v.cuda().transpose(0, 1).contiguous().transpose(0, 1)), ValueError), (dict(seq_lens=_i32(lens).cpu()), ValueError),
+                     (dict(out=torch.zeros(q.shape, device="cuda", dtype=torch.float16)), ValueError),
+                     (dict(workspace=torch.empty(512, dtype=torch.uint8, device="cuda")), tq4.TQ4Error)):
+        with pytest.raises(err):
+            ctx.prefill_attention_ragged(**{**ok, **bad})
+    none = ctx.prefill_attention_ragged(**{**ok, "q": q.cuda()[:0], "k_new": k.cuda()[:0], "v_new": v.cuda()[:0]})
+    assert none.shape[0] == 0 and ctx.status() == tq4.TQ4_OK
+
+
+def test_a_run_of_the_step(ctx):
+    """Three steps of four requests: plan, rotary append, then the chunk attention; the last step also as a
+    windowed decode. One request finds no page in the last step. Pool, tables and outputs follow the oracle."""
+    rng = np.random.default_rng(14)
+    signs, c = I.signs(CFG), O.codebook()[0]
+    n_req, max_pages, n_pages, window, sinks, rot = 4, 4, 7, 200, 3, 64
+    sections = [12, 10, 10]
+    free = rng.permutation(n_pages).astype(np.int64)
+    table = ctx.rope_table(3000, rot, 1e6)
+    cs_all = table.cpu().double().numpy()
+    tab = np.full((n_req, max_pages), -1, np.int64)
+    opool = O.new_pool(n_pages)
+    pool, dtab = tq4.Context.new_pool(n_pages), _i32(tab)
+    past = np.zeros(n_req, np.int64)
+    ws = ctx.prefill_ragged_workspace(n_req, 700, max_pages, window, sinks)
+    for step, new in enumerate(([300, 40, 0, 260], [5, 216, 400, 1], [1, 1, 1, 1])):
+        rows = sum(new) + 3
+        tab, cu, lens, pos, slot, taken, codes = S.plan_step(past, new, free, tab, n_pages, rows)
+        got = ctx.plan_step(_i32(past), _i32(new), _i32(free), dtab, n_pages, max_tok=rows)
+        torch.cuda.synchronize()
+        assert [x.cpu().tolist() for x in (dtab, *got)] == [x.tolist() for x in (tab, cu, lens, pos, slot)] + [[taken]]
+        assert ctx.status() == (tq4.TQ4_ERR_NO_PAGES if "pages" in codes else tq4.TQ4_OK)
+        assert ("pages" in codes) == (step == 2)
+        free = free[taken:]
+        qkv = torch.from_numpy(rng.normal(size=(rows, 32 * 256)).astype(np.float32)).bfloat16()
+        q, k, v = qkv[:, :6144].view(rows, 24, 256), qkv[:, 6144:7168].view(rows, 4, 256), qkv[:, 7168:].view(rows, 4, 256)
+        axes = np.stack([pos, pos // 2, pos % 50])
+        dev = qkv.cuda()
+        dq, dk, dv = dev[:, :6144].view(rows, 24, 256), dev[:, 6144:7168].view(rows, 4, 256), dev[:, 7168:].view(rows, 4, 256)
+        qr, kr = torch.zeros((rows, 24, 256), dtype=torch.bfloat16, device="cuda"), torch.zeros((rows, 4, 256), dtype=torch.bfloat16, device="cuda")
+        ctx.rope_append(pool, dq, dk, dv, _i32(axes), table, got[3], sections=sections, q_out=qr, k_out=kr)
+        cs = cs_all[axes[S.rope_axes(rot // 2, sections, False)].T, np.arange(rot // 2)]
+        S.store(opool, slot, S.rope_turn(k.double().numpy(), cs[..., 0], cs[..., 1], False), v.double().numpy(), signs, c)
+        assert np.array_equal(pool.cpu().numpy(), opool)
+        out = ctx.prefill_attention_ragged(pool, qr, kr, dv.contiguous(), got[0], got[1], dtab, window, sinks, SCALE, out_dtype=torch.float32, workspace=ws)
+        torch.cuda.synchronize()
+        assert ctx.status() == tq4.TQ4_OK
+        exp = S.prefill_attention_ragged(opool, tab, lens, cu, qr.double().cpu().numpy(), kr.double().cpu().numpy(), v.double().numpy(), window, sinks,
+                                         SCALE, signs, c)
+        assert_close(out[:cu[-1]], exp[:cu[-1]])
+        past = np.where(lens > 0, lens, past)
+    dec = ctx.decode_attention_window(pool, qr[:4].view(4, 1, 24, 256), dtab, got[1], window, sinks, SCALE, out_dtype=torch.float32)
+    exp = S.decode_attention_window(opool, tab, lens, qr[:4].view(4, 1, 24, 256).double().cpu().numpy(), window, sinks, SCALE, signs, c)
+    assert_close(dec, exp)
+    assert (lens == 0).any() and (lens > 0).any() and ctx.status() == tq4.TQ4_OK

@@ -3,10 +3,14 @@
 Tolerances. fp32 results carry every operand as an f16 hi + lo pair: the library's fp32 bound
 (1e-4 absolute, for values of size 1). bf16 results: half a bf16 step (2^-8 |o|), and three
 independent f16 roundings (the scores' operands, the weights, the centroids), each of at most
-2^-11 relative, of root mean square at most 2^-12 of a value's size v = norm / 16: six of their
-joint standard deviations, 6 sqrt(3) 2^-12 v, bound an element, and over a whole result the
-root mean square error stays below the rounding's own 2^-8 / sqrt(12) plus sqrt(3) 2^-12,
-together 2^-9 of the root mean square value with room of a fifth."""
+2^-11 relative, of root mean square at most 2^-12. Those of the weights and the centroids err by
+that share of a value's size v = norm / 16: 6 sqrt(3) 2^-12 v covers them. That of the scores: two
+operands, so a score is off by sqrt(2) 2^-12 s (root mean square; s = the norm of the products'
+vector, at most 2 here), and the result by sum p_j ds_j (v_j - o), at most for two positions of equal
+weight, 1/4 (ds_1 - ds_2) (v_1 - v_2): six deviations of ds_1 - ds_2, 6 sqrt(2) sqrt(2) 2^-12 2, times
+a difference of two coordinates of five times their size, 5 v, times 1/4: 30 * 2^-12 v. Over a whole
+result the root mean square error stays below the rounding's own 2^-8 / sqrt(12) plus
+sqrt(3) 2^-12, together 2^-9 of the root mean square value with room of a fifth."""
 import numpy as np
 import pytest
 
@@ -60,6 +64,10 @@ def check(got, exp, v_size=2.0):
     return got, err
 
 
+def element_tolerance(exp, v_size=2.0):
+    return 2.0 ** -8 * np.abs(exp) + (6 * 3 ** 0.5 + 30) * 2.0 ** -12 * v_size
+
+
 def assert_close(out, exp, v_size=2.0, scale=SCALE):
     got, err = check(out, exp)
     assert np.isfinite(got).all()
@@ -68,7 +76,7 @@ def assert_close(out, exp, v_size=2.0, scale=SCALE):
         # absolute error d of a score is a relative error d of its weight: at 16 times the scale the error is 16 times it
         assert err.max() <= 1e-4 * max(1.0, abs(scale) / SCALE), err.max()
     else:
-        assert (err <= 2.0 ** -8 * np.abs(exp) + 6 * 3 ** 0.5 * 2.0 ** -12 * v_size).all(), err.max()
+        assert (err <= element_tolerance(exp, v_size)).all(), err.max()
         rms = lambda a: np.sqrt(np.mean(np.square(a)))  # noqa: E731
         if exp.any():
             assert rms(err) <= 1.2 * 2.0 ** -9 * rms(exp)
