@@ -449,6 +449,12 @@ int tq4_ctx_create(const int8_t* signs, tq4_ctx** out) {
   if (e == cudaSuccess) e = set_decode_attrs<3, 3, true>();
   if (e == cudaSuccess) e = tq4::prefill_tc_set_attrs();
   if (e == cudaSuccess) e = cudaMemcpyToSymbol(tq4::g_boundaries64, ctx->boundaries, sizeof(ctx->boundaries));
+  float cells[32];
+  if (!tq4::make_cells(ctx->boundaries, cells)) {
+    delete ctx;
+    return TQ4_ERR_UNSUPPORTED;
+  }
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(tq4::g_cells, cells, sizeof(cells));
   if (e == cudaSuccess) e = tq4::plan_set_attrs();
   if (e == cudaSuccess) e = tq4::window_set_attrs();
   if (e == cudaSuccess) e = tq4::ragged_set_attrs();

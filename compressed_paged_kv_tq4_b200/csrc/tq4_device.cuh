@@ -80,12 +80,9 @@ __device__ __forceinline__ void warp_fwht256(float v[8]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
-    const bool upper = (lane & m) != 0;
+    const float own = (lane & m) ? -1.0f : 1.0f;   // the upper lane takes other - own: one fused step, exact by +-1
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float o = __shfl_xor_sync(0xffffffffu, v[i], m);
-      v[i] = upper ? (o - v[i]) : (v[i] + o);
-    }
+    for (int i = 0; i < 8; ++i) v[i] = fmaf(own, v[i], __shfl_xor_sync(0xffffffffu, v[i], m));
   }
 }
 

@@ -9,6 +9,8 @@
 // admission that these maps follow.
 #pragma once
 #include <algorithm>
+#include <cmath>
+#include <cstring>
 
 #include "tq4_device.cuh"
 #include "tq4_encode.cuh"
@@ -192,19 +194,49 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float2* table, int64_t 
 // Quantiser decisions equal the 64-bit definition. The 32-bit path bounds its own
 // error: with u = 2^-24 and ||x||_1 <= 16 ||x||_2, the rotation of a pair adds 3 u,
 // the norm 9 u (times |y| <= 0.16 next to a boundary), the scaling u and the eight
-// Hadamard levels 8 u of ||x||_1 / 16, together under 8e-7 of the unit vector. A
-// vector with a coordinate within 1e-6 of a boundary (one in ~40 of Gaussian ones),
-// or whose norm lies within 6e-7 (relative) of an fp16 rounding midpoint, is redone
-// in 64 bits by the whole warp.
+// Hadamard levels 8 u of ||x||_1 / 16, together under 8e-7 of the unit vector; a cell's
+// boundary (below) is off by at most 2.3e-7. A vector with a coordinate within 1.25e-6 of
+// a boundary (one in ~30 of Gaussian ones), or whose norm lies within 6e-7 (relative) of
+// an fp16 rounding midpoint, is redone in 64 bits by its warp.
 //
-// One CTA of 12 warps per token: warps 0-3 six query heads each (their six row loads
-// fly together), warps 4-7 the keys, 8-11 the values: an encode costs about as many
-// instructions as six rotations, so the three groups end together.
+// The quantiser finds the cell of width 1/64 around y's nearest multiple of 1/64: no cell
+// holds two boundaries, and none lies within 1e-4 of a cell's edge (both checked when the
+// table is made), so one comparison decides and its distance is the nearest boundary's
+// wherever that matters. Against 15 comparisons a coordinate (480 instructions a vector)
+// this takes 80, and the lookup is a shuffle: lane l holds cell l.
+//
+// One CTA of 8 warps per token: warps 0-3 six query heads each, 4-5 two keys, 6-7 two
+// values, so that all end together; a row's loads go out before the position's.
 // --------------------------------------------------------------------------
-constexpr int kRopeWarps = 12;
-constexpr float kRopeNear = 1e-6f;      // coordinates closer to a boundary are decided in 64 bits
+constexpr int kRopeWarps = 8;
+constexpr float kRopeNear = 1.25e-6f;   // coordinates closer to a boundary are decided in 64 bits
 constexpr float kRopeNormNear = 6e-7f;  // and norms closer (relative) to an fp16 midpoint
 __constant__ double g_boundaries64[15]; // decision boundaries in 64 bits
+// cell l: y nearest to (l - 16) / 64; its boundary (1000: none), the index below it in the low 4 bits
+__device__ float g_cells[32];
+constexpr float kCellClamp = 11.0f / 64.0f;   // the outermost cells in use
+
+// Fills cells from the 64-bit boundaries; false if they do not fit the scheme.
+inline bool make_cells(const double* b, float* cells) {
+  for (int l = 0; l < 32; ++l) {
+    const double lo = (l - 16.5) / 64.0, hi = (l - 15.5) / 64.0;
+    int below = 0, in = -1;
+    for (int j = 0; j < 15; ++j) {
+      if (std::fabs(b[j] - lo) < 1e-4 || std::fabs(b[j]) > kCellClamp) return false;
+      if (b[j] < lo) ++below;
+      else if (b[j] < hi) {
+        if (in >= 0) return false;
+        in = j;
+      }
+    }
+    const float v = in >= 0 ? float(b[in]) : 1000.0f;
+    uint32_t bits;
+    std::memcpy(&bits, &v, 4);
+    bits = (bits & ~15u) | uint32_t(below);
+    std::memcpy(cells + l, &bits, 4);
+  }
+  return true;
+}
 
 struct RopeParams {
   uint8_t* pool;
@@ -228,73 +260,44 @@ struct RopeParams {
   int* status;
 };
 
-// 8 elements; plain loads, since q_out may be q itself
+// 8 elements of a row as they lie in memory; plain loads, since an output may be its input
 template <typename T>
-__device__ __forceinline__ void load8_rw(const T* src, float v[8]);
+struct Raw8;
 template <>
-__device__ __forceinline__ void load8_rw<float>(const float* src, float v[8]) {
-  const float4 a = reinterpret_cast<const float4*>(src)[0], b = reinterpret_cast<const float4*>(src)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8_rw<uint16_t>(const uint16_t* src, float v[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(src);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* src) {
+    a = reinterpret_cast<const float4*>(src)[0];
+    b = reinterpret_cast<const float4*>(src)[1];
   }
-}
-__device__ __forceinline__ void store8_bf16(uint16_t* dst, const float v[8]) {
+  __device__ __forceinline__ void get(float v[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+template <>
+struct Raw8<uint16_t> {
+  uint4 a;
+  __device__ __forceinline__ void load(const uint16_t* src) { a = *reinterpret_cast<const uint4*>(src); }
+  __device__ __forceinline__ void get(float v[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
+__device__ __forceinline__ uint4 pack8_bf16(const float v[8]) {
   uint32_t pk[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
     pk[i] = *reinterpret_cast<const uint32_t*>(&b2);
   }
-  *reinterpret_cast<uint4*>(dst) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+  return make_uint4(pk[0], pk[1], pk[2], pk[3]);
 }
-
-// The encode of one vector in 64 bits (x: the rotated vector's coordinates 8 lane ..).
-__device__ __noinline__ void encode_vector_warp64(const double* x, uint32_t sb, uint32_t& word, uint16_t& norm) {
-  const int lane = threadIdx.x & 31;
-  double ss = 0.0, y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fma(x[i], x[i], ss);
-#pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-  const double n = sqrt(ss);
-  word = 0;
-  norm = __half_as_ushort(__double2half(n));
-  if (!(n > 0.0)) return;   // the same in every lane
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = ((sb >> i) & 1u) ? -x[i] / n : x[i] / n;
-#pragma unroll
-  for (int h = 1; h < 8; h <<= 1)
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if ((i & h) == 0) {
-        const double a = y[i], b = y[i + h];
-        y[i] = a + b;
-        y[i + h] = a - b;
-      }
-#pragma unroll
-  for (int m = 1; m < 32; m <<= 1)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const double o = __shfl_xor_sync(0xffffffffu, y[i], m);
-      y[i] = (lane & m) ? o - y[i] : y[i] + o;
-    }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t idx = 0;
-#pragma unroll
-    for (int j = 0; j < 15; ++j) idx += (y[i] * 0.0625 > g_boundaries64[j]) ? 1u : 0u;
-    word |= idx << (4 * i);
-  }
-}
+__device__ __forceinline__ void store8_bf16(uint16_t* dst, const float v[8]) { *reinterpret_cast<uint4*>(dst) = pack8_bf16(v); }
 
 // Rotation angles of one lane: c[i], s[i] for its coordinates 8 lane + i (halves: one
 // frequency per coordinate; adjacent: one per pair, in entries 0-3). partner: the lane
@@ -320,25 +323,38 @@ __device__ __forceinline__ bool load_angles(const RopeParams& p, int tok, LaneAn
   const int m = half >> 3;                 // lanes per half
   const int f0 = p.adjacent ? 4 * lane : 8 * (lane < m ? lane : lane - m);
   a.partner = p.adjacent || !a.active ? lane : lane < m ? lane + m : lane - m;
+  const float sgn = !p.adjacent && lane < m ? -1.f : 1.f;   // first half: x cos - partner sin
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     a.c[i] = 1.f;
     a.s[i] = 0.f;
-    if (a.active && i < per) {
-      const int f = f0 + i;
-      int32_t at = pos[0];
-      if (p.n_axes > 1) {
-        uint32_t wa = p.axis[0];
-#pragma unroll
-        for (int k = 1; k < 8; ++k) wa = (f >> 4) == k ? p.axis[k] : wa;
-        const uint32_t ax = (wa >> (2 * (f & 15))) & 3u;
-        at = ax == 0 ? pos[0] : ax == 1 ? pos[1] : pos[2];
-      }
-      const float2 cs = __ldg(p.table + int64_t(at) * half + f);
-      a.c[i] = cs.x;
-      a.s[i] = !p.adjacent && lane < m ? -cs.y : cs.y;   // first half: x cos - partner sin
-    }
   }
+  if (!a.active) return true;
+  if (p.n_axes == 1) {   // consecutive entries of one row, 16 bytes at a time
+    const float4* src = reinterpret_cast<const float4*>(p.table + int64_t(pos[0]) * half + f0);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+      if (i < per) {
+        const float4 cs = __ldg(src + i / 2);
+        a.c[i] = cs.x;
+        a.s[i] = sgn * cs.y;
+        a.c[i + 1] = cs.z;
+        a.s[i + 1] = sgn * cs.w;
+      }
+    return true;
+  }
+  uint32_t wa = 0;   // a lane's frequencies lie in one word
+#pragma unroll
+  for (int k = 0; k < 8; ++k) wa = (f0 >> 4) == k ? p.axis[k] : wa;
+  wa >>= 2 * (f0 & 15);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < per) {
+      const uint32_t ax = (wa >> (2 * i)) & 3u;
+      const float2 cs = __ldg(p.table + int64_t(ax == 0 ? pos[0] : ax == 1 ? pos[1] : pos[2]) * half + f0 + i);
+      a.c[i] = cs.x;
+      a.s[i] = sgn * cs.y;
+    }
   return true;
 }
 __device__ __forceinline__ void rotate8(const LaneAngles& a, bool adjacent, float x[8]) {
@@ -360,117 +376,186 @@ __device__ __forceinline__ void rotate8(const LaneAngles& a, bool adjacent, floa
   }
 }
 
+// Key or value vector (kv, head) of a token again, from its row, in 64 bits.
 template <typename T>
-__global__ void __launch_bounds__(32 * kRopeWarps) rope_append_kernel(const RopeParams p) {
+__device__ __noinline__ void encode_again64(const RopeParams& p, int tok, int kv, int head, uint32_t& word, uint16_t& norm) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t sb = lane_sign_bits(p.signs);
+  float raw[8];
+  Raw8<T> row;
+  row.load(static_cast<const T*>(kv ? p.v : p.k) + int64_t(tok) * (kv ? p.v_stride : p.k_stride) + head * kD + lane * 8);
+  row.get(raw);
+  double y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = raw[i];
+  if (kv == 0) {
+    LaneAngles a;
+    load_angles(p, tok, a);
+    if (p.adjacent) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const double u = raw[2 * j], v = raw[2 * j + 1], c = a.c[j], s = a.s[j];
+        if (a.active) {
+          y[2 * j] = u * c - v * s;
+          y[2 * j + 1] = v * c + u * s;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float o = __shfl_sync(0xffffffffu, raw[i], a.partner);
+        if (a.active) y[i] = double(raw[i]) * double(a.c[i]) + double(o) * double(a.s[i]);
+      }
+    }
+  }
+  double ss = 0.0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) ss = fma(y[i], y[i], ss);
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+  const double n = sqrt(ss);
+  word = 0;
+  norm = __half_as_ushort(__double2half(n));
+  if (!(n > 0.0)) return;   // the same in every lane
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = ((sb >> i) & 1u) ? -y[i] / n : y[i] / n;
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((i & h) == 0) {
+        const double a = y[i], b = y[i + h];
+        y[i] = a + b;
+        y[i + h] = a - b;
+      }
+#pragma unroll 1
+  for (int m = 1; m < 32; m <<= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const double o = __shfl_xor_sync(0xffffffffu, y[i], m);
+      y[i] = (lane & m) ? o - y[i] : y[i] + o;
+    }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t idx = 0;
+#pragma unroll
+    for (int j = 0; j < 15; ++j) idx += (y[i] * 0.0625 > g_boundaries64[j]) ? 1u : 0u;
+    word |= idx << (4 * i);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kRopeWarps, 3) rope_append_kernel(const __grid_constant__ RopeParams p) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int tok = blockIdx.x;
+  const float cell = g_cells[lane];
   pdl_wait();
   pdl_launch_dependents();
   const int64_t slot = __ldg(p.slots + tok);
-  if (slot < 0) return;   // padding, or a refused request: every row of it is left as it was
-  if (slot >= int64_t(p.num_pages) * kPage) {
-    if (threadIdx.x == 0) record_error(p.status, TQ4_ERR_PAGE_RANGE);
-    return;
-  }
-  LaneAngles a;
-  if (w < 8 && !load_angles(p, tok, a)) {
-    if (threadIdx.x == 0) record_error(p.status, TQ4_ERR_SEQ);
-    return;
-  }
   const bool adjacent = p.adjacent != 0;
+  constexpr int kBatch = sizeof(T) == 2 ? kGroup : kGroup / 2;   // query rows in flight
   if (w < 4) {
     if (!p.q) return;
-    float x[kGroup][8];
     const T* src = static_cast<const T*>(p.q) + int64_t(tok) * p.q_stride + w * kGroup * kD + lane * 8;
+    uint16_t* dst = p.q_out + (int64_t(tok) * kHq + w * kGroup) * kD + lane * 8;
+    Raw8<T> raw[kBatch];
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j) load8_rw<T>(src + j * kD, x[j]);
+    for (int j = 0; j < kBatch; ++j) raw[j].load(src + j * kD);
+    if (slot < 0 || slot >= int64_t(p.num_pages) * kPage) return;   // see below
+    LaneAngles a;
+    if (!load_angles(p, tok, a)) return;
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j) {
-      rotate8(a, adjacent, x[j]);
-      store8_bf16(p.q_out + (int64_t(tok) * kHq + w * kGroup + j) * kD + lane * 8, x[j]);
+    for (int j0 = 0; j0 < kGroup; j0 += kBatch) {
+      if (j0 > 0) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) raw[j].load(src + (j0 + j) * kD);
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        float x[8];
+        raw[j].get(x);
+        rotate8(a, adjacent, x);
+        store8_bf16(dst + (j0 + j) * kD, x);
+      }
     }
     return;
   }
-  const int kv = (w - 4) >> 2, head = w & 3;
-  if (kv == 1) {   // values are not rotated; their warps check the positions too, so that a
-    bool ok = true; // bad one leaves the whole token unwritten
+  const int kv = (w - 4) >> 1, head0 = 2 * (w & 1);
+  Raw8<T> raw[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    raw[j].load(static_cast<const T*>(kv ? p.v : p.k) + int64_t(tok) * (kv ? p.v_stride : p.k_stride) + (head0 + j) * kD + lane * 8);
+  if (slot < 0) return;   // padding, or a refused request: every row of it is left as it was
+  if (slot >= int64_t(p.num_pages) * kPage) {
+    if (w == 4 && lane == 0) record_error(p.status, TQ4_ERR_PAGE_RANGE);
+    return;
+  }
+  float y[2][8];
+  raw[0].get(y[0]);
+  raw[1].get(y[1]);
+  uint4 turned[2];
+  if (kv == 0) {
+    LaneAngles a;
+    if (!load_angles(p, tok, a)) {
+      if (w == 4 && lane == 0) record_error(p.status, TQ4_ERR_SEQ);
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      rotate8(a, adjacent, y[j]);
+      turned[j] = pack8_bf16(y[j]);
+    }
+  } else {   // values are not rotated; their warps check the positions too, so that a bad one leaves the whole token unwritten
+    bool ok = true;
     for (int x = 0; x < p.n_axes; ++x) {
       const int32_t at = __ldg(p.pos + int64_t(x) * p.n_tok + tok);
       ok &= at >= 0 && at < p.table_len;
     }
     if (!ok) return;
   }
-  float raw[8], x[8];
-  load8_rw<T>(static_cast<const T*>(kv ? p.v : p.k) + int64_t(tok) * (kv ? p.v_stride : p.k_stride) + head * kD + lane * 8, raw);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = raw[i];
-  if (kv == 0) {
-    rotate8(a, adjacent, x);
-    if (p.k_out) store8_bf16(p.k_out + (int64_t(tok) * kHkv + head) * kD + lane * 8, x);
-  }
   const uint32_t sb = lane_sign_bits(p.signs);
-  float ss = 0.f;
+  uint8_t* page = p.pool + (slot >> 8) * kPageBytes;
+  uint32_t word[2];
+  uint16_t norm[2];
+  bool redo[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+  for (int j = 0; j < 2; ++j) {
+    float ss = 0.f;
 #pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-  const float n = sqrtf(ss);
-  uint32_t word = 0;
-  uint16_t norm = __half_as_ushort(__float2half_rn(n));
-  // sums of squares outside [2^-100, 2^126] (and NaN) have lost digits in 32 bits
-  bool redo = ss != 0.f && !(ss > 0x1p-100f && ss < 0x1p126f);
-  redo |= __half_as_ushort(__float2half_rn(n * (1.f - kRopeNormNear))) != __half_as_ushort(__float2half_rn(n * (1.f + kRopeNormNear)));
-  if (!redo && ss > 0.f) {
+    for (int i = 0; i < 8; ++i) ss = fmaf(y[j][i], y[j][i], ss);
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+    const float n = sqrtf(ss);
+    norm[j] = __half_as_ushort(__float2half_rn(n));
+    // sums of squares outside [2^-100, 2^126] (and NaN) have lost digits in 32 bits
+    redo[j] = !(ss > 0x1p-100f && ss < 0x1p126f);
+    redo[j] |= __half_as_ushort(__float2half_rn(n * (1.f - kRopeNormNear))) != __half_as_ushort(__float2half_rn(n * (1.f + kRopeNormNear)));
     const float inv = 1.0f / n;
-    float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = apply_sign(x[i] * inv, sb, i);
-    warp_fwht256(y);
+    for (int i = 0; i < 8; ++i) y[j][i] = apply_sign(y[j][i] * inv, sb, i);
+    warp_fwht256(y[j]);
     float near = 1.f;
+    word[j] = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float yi = y[i] * 0.0625f;
-      uint32_t idx = 0;
-#pragma unroll
-      for (int j = 0; j < 15; ++j) {
-        const float d = yi - g_codebook.b[j];
-        idx += d > 0.f ? 1u : 0u;
-        near = fminf(near, fabsf(d));
-      }
-      word |= idx << (4 * i);
+      const float yi = y[j][i] * 0.0625f;
+      // 1.5 * 2^23 + 16 + 64 y: rounded to a whole number, whose low bits are the cell
+      const int l = __float_as_int(fmaf(fminf(fmaxf(yi, -kCellClamp), kCellClamp), 64.f, 12582912.f + 16.f));
+      const float b = __shfl_sync(0xffffffffu, cell, l);
+      const float d = yi - b;
+      near = fminf(near, fabsf(d));
+      word[j] |= ((__float_as_uint(b) & 15u) + (d > 0.f ? 1u : 0u)) << (4 * i);
     }
-    redo = __any_sync(0xffffffffu, near < kRopeNear);
-  } else if (ss == 0.f) {   // all zeros, or squares below the fp32 range
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) any |= x[i] != 0.f;
-    redo = __any_sync(0xffffffffu, any);
+    redo[j] |= __any_sync(0xffffffffu, near < kRopeNear) != 0;
   }
-  if (redo) {   // uniform in the warp
-    double xd[8];
-    if (kv == 1) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) xd[i] = raw[i];
-    } else if (adjacent) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const double u = raw[2 * j], v = raw[2 * j + 1], c = a.c[j], s = a.s[j];
-        xd[2 * j] = a.active ? u * c - v * s : u;
-        xd[2 * j + 1] = a.active ? v * c + u * s : v;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float o = __shfl_sync(0xffffffffu, raw[i], a.partner);
-        xd[i] = a.active ? double(raw[i]) * double(a.c[i]) + double(o) * double(a.s[i]) : double(raw[i]);
-      }
-    }
-    encode_vector_warp64(xd, sb, word, norm);
+  for (int j = 0; j < 2; ++j) {
+    if (redo[j]) encode_again64<T>(p, tok, kv, head0 + j, word[j], norm[j]);   // uniform in the warp
+    const int at = (head0 + j) * kPage + int(slot & (kPage - 1));
+    reinterpret_cast<uint32_t*>(page + (kv ? kVWords : kKWords))[at * kWords + lane] = word[j];
+    if (lane == 0) reinterpret_cast<uint16_t*>(page + (kv ? kVNorms : kKNorms))[at] = norm[j];
+    if (kv == 0 && p.k_out) *reinterpret_cast<uint4*>(p.k_out + (int64_t(tok) * kHkv + head0 + j) * kD + lane * 8) = turned[j];
   }
-  uint8_t* page = p.pool + (slot >> 8) * kPageBytes;
-  const int at = head * kPage + int(slot & (kPage - 1));
-  reinterpret_cast<uint32_t*>(page + (kv ? kVWords : kKWords))[at * kWords + lane] = word;
-  if (lane == 0) reinterpret_cast<uint16_t*>(page + (kv ? kVNorms : kKNorms))[at] = norm;
 }
 
 // --------------------------------------------------------------------------

@@ -532,22 +532,58 @@ def _need_cuda(*ts):
             raise ValueError("TQ4 kernels take CUDA tensors")
 
 
-def _need(name, t, dtype, shape, device, rows=False):
-    """A CUDA tensor of this dtype (or one of several), shape (None: any length) and device;
-    contiguous, or with rows=True of contiguous rows any distance apart."""
+def _need(name, t, dtype, shape, device):
+    """A contiguous CUDA tensor of this dtype, shape and device (a step makes a dozen of these checks a
+    call: the good case is one expression)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+        return
+    _refuse(name, t, (dtype,), shape, device, False)
+
+
+def _need_rows(name, t, dtype, shape, device):
+    """The same, but the rows t[i], each contiguous, may be any distance apart."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.stride()[1:] == (HEAD_DIM, 1) and
+            t.device == device):
+        return
+    _refuse(name, t, (dtype,), shape, device, True)
+
+
+def _refuse(name, t, dtypes, shape, device, rows):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}")
-    if t.dim() != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if not (t[:1].is_contiguous() if rows else t.is_contiguous()):
+    if not (rows and t[:1].is_contiguous()) and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
+def _out_code(out):
+    code = _OUT_CODES.get(out.dtype)
+    if code is None:
+        raise ValueError(f"out has dtype {out.dtype}, not float32 or bfloat16")
+    return code
+
+
+def _pool_pages(pool, device):
+    if not (isinstance(pool, torch.Tensor) and pool.dtype is torch.uint8 and pool.is_contiguous() and pool.device == device):
+        raise ValueError(f"pool must be a contiguous uint8 tensor on {device}")
+    return pool.numel() // PAGE_BYTES
+
+
 _OUT_CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _scratch(workspace, device):
+    """Address and bytes of a caller's workspace (or none)."""
+    if workspace is None:
+        return None, 0
+    if not (workspace.is_contiguous() and workspace.device == device):
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 class Context:
@@ -860,23 +896,38 @@ class Context:
             if tok_pos is None:
                 raise ValueError("give max_tok or tok_pos")
             max_tok = tok_pos.numel()
-        new = lambda size, dtype: torch.empty(size, dtype=dtype, device=dev)  # noqa: E731
-        cu_tok = new(n + 1, torch.int32) if cu_tok is None else cu_tok
-        seq_lens = new(n, torch.int32) if seq_lens is None else seq_lens
-        tok_pos = new(max_tok, torch.int32) if tok_pos is None else tok_pos
-        tok_slot = new(max_tok, torch.int64) if tok_slot is None else tok_slot
-        taken = new(1, torch.int32) if taken is None else taken
-        for name, t, dtype, shape in (("past_lens", past_lens, torch.int32, (n,)), ("new_lens", new_lens, torch.int32, (n,)),
-                                      ("free_pages", free_pages, torch.int32, (None,)),
-                                      ("page_tables", page_tables, torch.int32, (n, None)),
-                                      ("cu_tok", cu_tok, torch.int32, (n + 1,)), ("seq_lens", seq_lens, torch.int32, (n,)),
-                                      ("tok_pos", tok_pos, torch.int32, (max_tok,)),
-                                      ("tok_slot", tok_slot, torch.int64, (max_tok,)), ("taken", taken, torch.int32, (1,))):
-            _need(name, t, dtype, shape, dev)
-        _check(tq4_plan_step(self.handle, past_lens, new_lens, n, free_pages, free_pages.numel(), num_pages, page_tables,
-                             page_tables.shape[1], cu_tok, seq_lens, tok_pos, tok_slot, max_tok, taken, stream),
+        i32, i64 = torch.int32, torch.int64
+        if cu_tok is None:
+            cu_tok = torch.empty(n + 1, dtype=i32, device=dev)
+        if seq_lens is None:
+            seq_lens = torch.empty(n, dtype=i32, device=dev)
+        if tok_pos is None:
+            tok_pos = torch.empty(max_tok, dtype=i32, device=dev)
+        if tok_slot is None:
+            tok_slot = torch.empty(max_tok, dtype=i64, device=dev)
+        if taken is None:
+            taken = torch.empty(1, dtype=i32, device=dev)
+        n_free, max_pages = free_pages.numel(), page_tables.shape[-1]
+        _need("past_lens", past_lens, i32, (n,), dev)
+        _need("new_lens", new_lens, i32, (n,), dev)
+        _need("free_pages", free_pages, i32, (n_free,), dev)
+        _need("page_tables", page_tables, i32, (n, max_pages), dev)
+        _need("cu_tok", cu_tok, i32, (n + 1,), dev)
+        _need("seq_lens", seq_lens, i32, (n,), dev)
+        _need("tok_pos", tok_pos, i32, (max_tok,), dev)
+        _need("tok_slot", tok_slot, i64, (max_tok,), dev)
+        _need("taken", taken, i32, (1,), dev)
+        _check(_lib.tq4_plan_step(self.handle, past_lens.data_ptr(), new_lens.data_ptr(), n, free_pages.data_ptr(), n_free,
+                                  num_pages, page_tables.data_ptr(), max_pages, cu_tok.data_ptr(), seq_lens.data_ptr(),
+                                  tok_pos.data_ptr(), tok_slot.data_ptr(), max_tok, taken.data_ptr(), self._stream(stream)),
                "tq4_plan_step")
         return cu_tok, seq_lens, tok_pos, tok_slot, taken
+
+    def _stream(self, stream):
+        """The raw stream of a call: the given one, or torch's current stream of the context's device."""
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.device.index)
+        return _stream(stream)
 
     def rope_table(self, table_len, rot, base, stream=None) -> torch.Tensor:
         """{cos, sin} of pos * base^(-2 i / rot): float32 [table_len, rot / 2, 2]."""
@@ -889,50 +940,58 @@ class Context:
         """Rotary positions on q [n, 24, 256] (or None) and k [n, 4, 256], then encode + append of k and
         v by slot. pos int32 [axes, n] or [n]; table float32 [len, rot / 2, 2]; sections: frequencies per
         axis; pairs "halves" or "adjacent". Returns q_out (bf16); k_out (bf16), if given, gets the turned keys."""
-        if pairs not in ("halves", "adjacent"):
+        dev, n, dtype = self.device, k.shape[0], k.dtype
+        if pairs != "halves" and pairs != "adjacent":
             raise ValueError("pairs must be 'halves' or 'adjacent'")
-        dev, n, both = self.device, k.shape[0], (torch.float32, torch.bfloat16)
-        if pos.dim() == 1:
-            pos = pos[None]
-        _need("pool", pool, torch.uint8, (None,), dev)
-        _need("k", k, both, (n, KV_HEADS, HEAD_DIM), dev, rows=True)
-        _need("v", v, k.dtype, (n, KV_HEADS, HEAD_DIM), dev, rows=True)
-        _need("pos", pos, torch.int32, (None, n), dev)
-        _need("table", table, torch.float32, (None, None, 2), dev)
+        code = _OUT_CODES.get(dtype)
+        if code is None:
+            raise ValueError("k must be float32 or bfloat16")
+        axes = 1 if pos.dim() == 1 else pos.shape[0]
+        length, half = table.shape[0], table.shape[1]
+        kv_shape = (n, KV_HEADS, HEAD_DIM)
+        num_pages = _pool_pages(pool, dev)
+        _need_rows("k", k, dtype, kv_shape, dev)
+        _need_rows("v", v, dtype, kv_shape, dev)
+        _need("pos", pos, torch.int32, (n,) if pos.dim() == 1 else (axes, n), dev)
+        _need("table", table, torch.float32, (length, half, 2), dev)
         _need("slots", slots, torch.int64, (n,), dev)
         if q is not None:
-            _need("q", q, k.dtype, (n, Q_HEADS, HEAD_DIM), dev, rows=True)
+            _need_rows("q", q, dtype, (n, Q_HEADS, HEAD_DIM), dev)
             if q_out is None:
                 q_out = torch.empty((n, Q_HEADS, HEAD_DIM), dtype=torch.bfloat16, device=dev)
             _need("q_out", q_out, torch.bfloat16, (n, Q_HEADS, HEAD_DIM), dev)
         elif q_out is not None:
             raise ValueError("q_out without q")
         if k_out is not None:
-            _need("k_out", k_out, torch.bfloat16, (n, KV_HEADS, HEAD_DIM), dev)
-        rot = 2 * table.shape[1]
+            _need("k_out", k_out, torch.bfloat16, kv_shape, dev)
         if sections is None:
-            if pos.shape[0] != 1:
+            if axes != 1:
                 raise ValueError("several axes need sections")
-            sections = [rot // 2]
-        if len(sections) != pos.shape[0]:
+            sections = (half,)
+        if len(sections) != axes:
             raise ValueError("one section per axis of pos")
-        step = lambda t, heads: heads * HEAD_DIM if t is None or n < 2 else t.stride(0)  # noqa: E731
-        _check(tq4_rope_append(self.handle, pool, pool.numel() // PAGE_BYTES, q, k, v, _OUT_CODES[k.dtype],
-                               step(q, Q_HEADS), step(k, KV_HEADS), step(v, KV_HEADS), n, pos, pos.shape[0],
-                               [int(x) for x in sections], interleaved, pairs == "adjacent", table, table.shape[0], rot,
-                               slots, q_out, k_out, stream), "tq4_rope_append")
+        sec = (_i32 * axes)(*sections)
+        many = n > 1   # a single row's stride says nothing
+        _check(_lib.tq4_rope_append(self.handle, pool.data_ptr(), num_pages, None if q is None else q.data_ptr(), k.data_ptr(),
+                                    v.data_ptr(), code, q.stride(0) if many and q is not None else Q_HEADS * HEAD_DIM,
+                                    k.stride(0) if many else KV_HEADS * HEAD_DIM, v.stride(0) if many else KV_HEADS * HEAD_DIM,
+                                    n, pos.data_ptr(), axes, sec, int(interleaved), int(pairs == "adjacent"), table.data_ptr(),
+                                    length, 2 * half, slots.data_ptr(), None if q_out is None else q_out.data_ptr(),
+                                    None if k_out is None else k_out.data_ptr(), self._stream(stream)), "tq4_rope_append")
         return q_out
 
     def reconstruct_slots(self, pool, slots, out_dtype=torch.float32, stream=None):
         """The stored K and V vectors of int64 slots [n]: two tensors [n, 4, 256] (zeros for negative slots)."""
-        if out_dtype not in _OUT_CODES:
+        code = _OUT_CODES.get(out_dtype)
+        if code is None:
             raise ValueError("out_dtype must be float32 or bfloat16")
-        _need("pool", pool, torch.uint8, (None,), self.device)
-        _need("slots", slots, torch.int64, (None,), self.device)
-        k = torch.empty((slots.numel(), KV_HEADS, HEAD_DIM), dtype=out_dtype, device=pool.device)
-        v = torch.empty_like(k)
-        _check(tq4_reconstruct_slots(self.handle, pool, pool.numel() // PAGE_BYTES, slots, slots.numel(), k, v,
-                                     _OUT_CODES[out_dtype], stream), "tq4_reconstruct_slots")
+        n = slots.numel()
+        num_pages = _pool_pages(pool, self.device)
+        _need("slots", slots, torch.int64, (n,), self.device)
+        kv = torch.empty((2, n, KV_HEADS, HEAD_DIM), dtype=out_dtype, device=self.device)
+        k, v = kv.unbind(0)
+        _check(_lib.tq4_reconstruct_slots(self.handle, pool.data_ptr(), num_pages, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
+                                          code, self._stream(stream)), "tq4_reconstruct_slots")
         return k, v
 
     def decode_window_workspace(self, n_req, n_q, max_pages, window, sinks, device="cuda") -> torch.Tensor:
@@ -943,21 +1002,22 @@ class Context:
                                 out_dtype=torch.bfloat16, workspace=None, stream=None):
         """decode_attention over a sliding window and the first `sinks` positions: q bf16
         [n_req, n_q, 24, 256], page_tables int32 [n_req, max_pages], seq_lens int32 [n_req] (0: padding, zeros)."""
-        dev, n_req, n_q = self.device, q.shape[0], q.shape[1]
-        _need("pool", pool, torch.uint8, (None,), dev)
-        _need("q", q, torch.bfloat16, (n_req, n_q, Q_HEADS, HEAD_DIM), dev)
-        _need("page_tables", page_tables, torch.int32, (n_req, None), dev)
+        dev = self.device
+        n_req, n_q = q.shape[0], q.shape[1]
+        shape, max_pages = (n_req, n_q, Q_HEADS, HEAD_DIM), page_tables.shape[-1]
+        num_pages = _pool_pages(pool, dev)
+        _need("q", q, torch.bfloat16, shape, dev)
+        _need("page_tables", page_tables, torch.int32, (n_req, max_pages), dev)
         _need("seq_lens", seq_lens, torch.int32, (n_req,), dev)
         if out is None:
-            out = torch.empty(q.shape, dtype=out_dtype, device=dev)
-        _need("out", out, tuple(_OUT_CODES), tuple(q.shape), dev)
-        max_pages = page_tables.shape[1]
+            out = torch.empty(shape, dtype=out_dtype, device=dev)
+        code = _out_code(out)
+        _need("out", out, out.dtype, shape, dev)
         if workspace is None and n_req > 0:
             workspace = self.decode_window_workspace(n_req, n_q, max_pages, window, sinks, dev)
-        _check(tq4_decode_attention_window(self.handle, pool, pool.numel() // PAGE_BYTES, q, page_tables, max_pages,
-                                           seq_lens, n_req, n_q, window, sinks, scale, out, _OUT_CODES[out.dtype],
-                                           workspace, workspace.numel() if workspace is not None else 0, stream),
-               "tq4_decode_attention_window")
+        _check(_lib.tq4_decode_attention_window(self.handle, pool.data_ptr(), num_pages, q.data_ptr(), page_tables.data_ptr(),
+                                                max_pages, seq_lens.data_ptr(), n_req, n_q, window, sinks, scale, out.data_ptr(),
+                                                code, *_scratch(workspace, dev), self._stream(stream)), "tq4_decode_attention_window")
         return out
 
     def prefill_ragged_workspace(self, n_req, n_tok, max_pages, window, sinks, out_dtype=torch.float32,
@@ -973,22 +1033,23 @@ class Context:
         [rows, 4, 256] (request r's rows are cu_tok[r] .. cu_tok[r + 1] - 1), seq_lens int32 [n_req] with the new
         positions, page_tables int32 [n_req, max_pages]. Rows behind the last request's are left as they were."""
         dev, rows, n_req = self.device, q.shape[0], seq_lens.numel()
-        _need("pool", pool, torch.uint8, (None,), dev)
-        _need("q", q, torch.bfloat16, (rows, Q_HEADS, HEAD_DIM), dev)
-        _need("k_new", k_new, torch.bfloat16, (rows, KV_HEADS, HEAD_DIM), dev)
-        _need("v_new", v_new, torch.bfloat16, (rows, KV_HEADS, HEAD_DIM), dev)
+        shape, kv_shape, max_pages = (rows, Q_HEADS, HEAD_DIM), (rows, KV_HEADS, HEAD_DIM), page_tables.shape[-1]
+        num_pages = _pool_pages(pool, dev)
+        _need("q", q, torch.bfloat16, shape, dev)
+        _need("k_new", k_new, torch.bfloat16, kv_shape, dev)
+        _need("v_new", v_new, torch.bfloat16, kv_shape, dev)
         _need("cu_tok", cu_tok, torch.int32, (n_req + 1,), dev)
         _need("seq_lens", seq_lens, torch.int32, (n_req,), dev)
-        _need("page_tables", page_tables, torch.int32, (n_req, None), dev)
+        _need("page_tables", page_tables, torch.int32, (n_req, max_pages), dev)
         if out is None:
-            out = torch.zeros(q.shape, dtype=out_dtype, device=dev)
-        _need("out", out, tuple(_OUT_CODES), tuple(q.shape), dev)
-        max_pages = page_tables.shape[1]
+            out = torch.zeros(shape, dtype=out_dtype, device=dev)
+        code = _out_code(out)
+        _need("out", out, out.dtype, shape, dev)
         if workspace is None and n_req > 0 and rows > 0:
             workspace = self.prefill_ragged_workspace(n_req, rows, max_pages, window, sinks, out.dtype, dev)
-        _check(tq4_prefill_attention_ragged(self.handle, pool, pool.numel() // PAGE_BYTES, q, k_new, v_new, rows, cu_tok,
-                                            seq_lens, page_tables, max_pages, n_req, window, sinks, scale, out,
-                                            _OUT_CODES[out.dtype], workspace,
-                                            workspace.numel() if workspace is not None else 0, stream),
+        _check(_lib.tq4_prefill_attention_ragged(self.handle, pool.data_ptr(), num_pages, q.data_ptr(), k_new.data_ptr(),
+                                                 v_new.data_ptr(), rows, cu_tok.data_ptr(), seq_lens.data_ptr(),
+                                                 page_tables.data_ptr(), max_pages, n_req, window, sinks, scale, out.data_ptr(),
+                                                 code, *_scratch(workspace, dev), self._stream(stream)),
                "tq4_prefill_attention_ragged")
         return out
