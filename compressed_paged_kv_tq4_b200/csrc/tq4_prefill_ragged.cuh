@@ -8,12 +8,13 @@
 // mechanism table row KVExec): o = R^T sum_j p_j R v_j / sum_j p_j, p_j = exp(scale R q . R k_j).
 //
 // Three launches.
-//   prep     every vector that some token sees becomes one f16 row of 512 B (and its norm one
-//            float): a cached vector its centroids c[idx] (the norm apart), a chunk vector R x
-//            brought to [0.5, 1) by a power of two (its norm). Rows of a request lie tile by
-//            tile, those of the sinks, then those of the window. The queries become rows R q,
-//            scaled likewise. One CTA also lays out the work: tiles per block of 256 query
-//            rows, their running sum, and where each CTA pair's share begins.
+//   prep     every vector that some token sees becomes one f16 row of 512 B: a key its rotated
+//            coordinates (a cached one norm * c[idx]), a value its direction, with its size one
+//            float beside it (a cached one c[idx] and the norm; a chunk's R v brought to
+//            [0.5, 1) by a power of two). Rows of a request lie tile by tile, those of the
+//            sinks, then those of the window. The queries become rows R q, scaled as values
+//            are. One CTA also lays out the work: tiles per block of 256 query rows, their
+//            running sum, and where each CTA pair's share begins.
 //   attend   one persistent CTA pair per two SMs. All tiles of all (KV head, row block) items
 //            stand in one line, of which each pair takes an equal part, so lengths, heads and
 //            chunk sizes of any mixture keep every SM busy to the end; an item that two pairs
@@ -24,13 +25,16 @@
 // cores then never wait for a lookup: tiles arrive by TMA, and the CTA is a plain pipeline.
 //
 // attend, per CTA (rank r of the pair holds query rows 128 r .. of the item's 256):
-//   warps 0-3  softmax, one thread per row: scores from TMEM, K norms, mask, running maximum
-//              (raised only when it grows by more than 2^4), P = p * n_v written over the
-//              scores as f16; the epilogue: O / l, R^T by in-register butterflies, out.
-//   warp 4     K tiles (its half of each tile's positions) and the norms
-//   warp 5     rank 0: issues every tcgen05.mma of the pair, QK(j) then PV(j - 1);
+//   warps 0-7  softmax: warps w and w + 4 share 32 rows, half of the columns each, one thread
+//              per row: scores from TMEM, mask, running maximum (exchanged through shared
+//              memory; raised only when it grows by more than 2^4), P = p * n_v written over
+//              the scores as f16; the epilogue: O / l, R^T by in-register butterflies, out.
+//   warp 8     K tiles (its half of each tile's positions) and the values' sizes
+//   warp 9     rank 0: issues every tcgen05.mma of the pair, QK(j) then PV(j - 1);
 //              rank 1: tells rank 0 when its own copies have landed
-//   warp 6     V tiles (its half of the dims)      warp 7  Q rows
+//   warp 10    V tiles (its half of the dims)      warp 11  Q rows
+// A vector with an infinity or a NaN (or too large for the rows) becomes a key row of NaN and a
+// value row of zeros: a mask takes its score away whole, so only those who see it feel it.
 // bf16 results: single f16 operands (queries, centroids, weights: each rounded once, 2^-11
 // relative), tiles of 128 positions, two stages. fp32 results (kExact): f16 hi + lo pairs,
 // S = Qh Kh + Ql Kh + Qh Kl, O = Ph Vh + Pl Vh + Ph Vl, tiles of 64 positions, one stage.
@@ -43,8 +47,8 @@
 
 namespace tq4 {
 
-constexpr int kRgThreads = 256;
-constexpr int kRgSoftWarps = 4, kRgKWarp = 4, kRgMmaWarp = 5, kRgVWarp = 6, kRgQWarp = 7;
+constexpr int kRgSoftWarps = 8, kRgKWarp = 8, kRgMmaWarp = 9, kRgVWarp = 10, kRgQWarp = 11;
+constexpr int kRgThreads = 32 * 12;
 constexpr int kRgNormSlots = 4;
 constexpr int kRgMinTiles = 256;      // positions: a pair's share is at least this many (a few tiles)
 template <bool kExact>
@@ -60,8 +64,10 @@ struct RgShape {
   static constexpr uint32_t kVPart = 2 * kVPanel;
   static constexpr uint32_t kKOff = kParts * kQPart;
   static constexpr uint32_t kVOff = kKOff + kStages * kParts * kKPart;
-  static constexpr uint32_t kNormOff = kVOff + kStages * kParts * kVPart;   // [slots][K, V][kTile] f32
-  static constexpr uint32_t kBarOff = kNormOff + kRgNormSlots * 2 * kTile * 4;
+  static constexpr uint32_t kNormOff = kVOff + kStages * kParts * kVPart;   // [slots][kTile] f32: sizes of the values
+  static constexpr uint32_t kMaxOff = kNormOff + kRgNormSlots * kTile * 4;   // [2][2 halves][128] f32: row maxima
+  static constexpr uint32_t kOkOff = kMaxOff + 2 * 2 * kPfRows * 4;          // [2][warps] u32: still at work
+  static constexpr uint32_t kBarOff = kOkOff + 2 * kRgSoftWarps * 4;
   static constexpr uint32_t kMiscOff = kBarOff + 256;         // [0] TMEM base, [1] abort
   static constexpr uint32_t kSmem = kMiscOff + 64 + 1024;     // + alignment slack
   static constexpr float kLazy = kExact ? 0.f : 4.f;           // P = p n_v / 16 <= 2^4 * 65504 / 16; fp32: p <= 1, P = p n_v
@@ -115,7 +121,7 @@ struct RaggedParams {
   __half* qr;         // [parts][4][6 n_tok][256]
   float* qfac;        // [4][6 n_tok]
   __half* rows;       // [parts][K, V][4][store_rows][256]
-  float* norms;       // [K, V][4][store_rows]
+  float* norms;       // [4][store_rows] sizes of the values
   int64_t store_rows;
   float* po;          // [2 max_pairs][256][256]
   float2* pml;        // [2 max_pairs][256]
@@ -150,7 +156,7 @@ inline RgLayout ragged_layout(int32_t num_sms, int32_t n_req, int32_t n_tok, int
   l.qr = take(size_t(parts) * kHq * n_tok * kD * 2);
   l.qfac = take(size_t(kHq) * n_tok * 4);
   l.rows = take(size_t(parts) * 2 * kHkv * l.store_rows * kD * 2);
-  l.norms = take(size_t(2) * kHkv * l.store_rows * 4);
+  l.norms = take(size_t(kHkv) * l.store_rows * 4);
   l.po = take(2 * pairs * 256 * kD * 4);
   l.pml = take(2 * pairs * 256 * 8);
   l.total = at;
@@ -188,7 +194,8 @@ __device__ __forceinline__ RgSpan rg_block_span(const RaggedParams& p, const RgR
 
 // --------------------------------------------------------------------------
 // prep. Every CTA scans the requests (as plan_step does); CTA 0 then lays out the work, the
-// others make rows: units of one (row tile, K or V, KV head) and of one token's queries.
+// others make rows: units of 32 positions of one (row tile, KV head), keys and values, and of one
+// token's queries.
 // --------------------------------------------------------------------------
 constexpr int kRgPrepThreads = 256;
 
@@ -210,11 +217,8 @@ __device__ __forceinline__ void rg_store_row(__half* dst, int64_t part_stride, c
     *reinterpret_cast<uint4*>(dst + part_stride + lane * 8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 }
-// R x * 16 of a bf16 vector, brought to [0.5, 1) by 2^-e; returns 2^e (0 for a zero vector). A vector
-// with an infinity or a NaN becomes zeros with the factor NaN, so that only those who see it feel it.
-__device__ __forceinline__ float rg_rotate(const uint16_t* src, uint32_t sb, float v[8]) {
-  const int lane = threadIdx.x & 31;
-  const uint4 raw = __ldg(reinterpret_cast<const uint4*>(src + lane * 8));
+// R x * 16 of a bf16 vector in v; returns the largest magnitude's bits (infinities and NaN above every number)
+__device__ __forceinline__ uint32_t rg_rotate(const uint4 raw, uint32_t sb, float v[8]) {
   const uint32_t ww[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -222,22 +226,22 @@ __device__ __forceinline__ float rg_rotate(const uint16_t* src, uint32_t sb, flo
     v[2 * i + 1] = apply_sign(__uint_as_float(ww[i] & 0xFFFF0000u), sb, 2 * i + 1);
   }
   warp_fwht256(v);
-  uint32_t top = 0;   // largest magnitude as bits: orders infinities and NaN above every number
+  uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (top >= 0x7F800000u) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    return __uint_as_float(0x7FC00000u);
-  }
-  if (top == 0) return 0.f;
+  return __reduce_max_sync(0xffffffffu, top);
+}
+// v brought to [0.5, 1) by 2^-e (zeros stay); returns 2^e
+__device__ __forceinline__ float rg_scale(uint32_t top, float v[8]) {
   const int e = min(max(int(top >> 23) - 126, -100), 126);
   const float down = __uint_as_float(uint32_t(127 - e) << 23);
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] *= down;
   return __uint_as_float(uint32_t(127 + e) << 23);
 }
+// below 2^15 * 16: a rotated coordinate (times 16) up to this fits an f16, and so does a value's size times
+// the largest weight, 2^4 / 16
+constexpr uint32_t kRgTop = 0x48FFFFFFu;
 
 template <bool kExact>
 __global__ void __launch_bounds__(kRgPrepThreads) ragged_prep_kernel(const RaggedParams p) {
@@ -245,16 +249,19 @@ __global__ void __launch_bounds__(kRgPrepThreads) ragged_prep_kernel(const Ragge
   constexpr int kTile = Sh::kTile;
   extern __shared__ int32_t prep_smem[];
   __shared__ int64_t tot[3][kRgPrepThreads / 32], carry[3];
-  __shared__ uint32_t pair_s[256];   // centroid pairs of a byte of codes: f16 hi
-  __shared__ uint32_t res_s[kExact ? 256 : 1];   // and lo
+  __shared__ uint32_t pair_s[256][8];   // centroid pairs of a byte of codes, f16 hi: 8 copies against bank conflicts
+  __shared__ uint32_t res_s[kExact ? 256 : 1][8];   // and lo
   __shared__ int32_t s_blocks, s_tiles;
   int32_t* const row0_s = prep_smem;             // [n_req]
   int32_t* const tile0_s = row0_s + p.n_req;     // [n_req]
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   {
     const uint2 c = lut_row(tid);
-    pair_s[tid] = c.x;
-    if constexpr (kExact) res_s[tid] = c.y;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      pair_s[tid][i] = c.x;
+      if constexpr (kExact) res_s[tid][i] = c.y;
+    }
   }
   if (tid < 3) carry[tid] = 0;
   pdl_wait();
@@ -374,7 +381,8 @@ __global__ void __launch_bounds__(kRgPrepThreads) ragged_prep_kernel(const Ragge
 
   // ---- rows
   const uint32_t sb = lane_sign_bits(p.signs);
-  const int64_t kv_units = int64_t(s_tiles) * 2 * kHkv;
+  constexpr int kQuarters = kTile / 32;
+  const int64_t kv_units = int64_t(s_tiles) * kHkv * kQuarters;
   const int32_t live = int32_t(min(max(int64_t(cu0) + carry[0], int64_t(0)), int64_t(p.n_tok)));   // rows of the last request end here
   const int64_t q_part = int64_t(kHq) * p.n_tok * kD, kv_part = int64_t(2) * kHkv * p.store_rows * kD;
   for (int64_t u = int64_t(blockIdx.x) - 1; u < kv_units + live; u += int64_t(gridDim.x) - 1) {
@@ -401,7 +409,8 @@ __global__ void __launch_bounds__(kRgPrepThreads) ragged_prep_kernel(const Ragge
           continue;
         }
         float v[8];
-        const float up = rg_rotate(p.q + (int64_t(tok) * kHq + hq) * kD, sb, v);
+        const uint32_t top = rg_rotate(__ldg(reinterpret_cast<const uint4*>(p.q + (int64_t(tok) * kHq + hq) * kD + lane * 8)), sb, v);
+        const float up = top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : rg_scale(top, v);   // (a row with a NaN is its own only)
         const int64_t row = int64_t(h) * kGroup * p.n_tok + int64_t(tok) * kGroup + (hq - h * kGroup);
         // the scores' factor is kept positive (the scale's sign goes into the row) and above zero,
         // so that a masked -infinity stays one
@@ -415,46 +424,97 @@ __global__ void __launch_bounds__(kRgPrepThreads) ragged_prep_kernel(const Ragge
       }
       continue;
     }
-    // one row tile of one KV head's keys or values
-    const int st = int(u >> 3), kv = int(u >> 2) & 1, h = int(u) & 3;
+    // 32 positions of a row tile, one KV head: four a warp, keys and values together
+    const int part = int(u % kQuarters), h = int((u / kQuarters) & 3), st = int(u / (kQuarters * kHkv));
     const int r = rg_last_at_most<int32_t>(tile0_s, p.n_req, st);   // requests without tiles share their next's tile0
     const int32_t T = p.seq_lens[r], row0 = p.cu[r], first = T - (p.cu[r + 1] - row0);
     const int32_t lo = max(0, first - p.window + 1);
     const RgSpan s = rg_span<kTile>(lo, T - 1, p.n_sink);
     const int local = st - tile0_s[r];
-    const int32_t pos0 = (local < s.sinks ? local : local + s.skip) * kTile;
+    const int32_t pos0 = (local < s.sinks ? local : local + s.skip) * kTile + 32 * part + 4 * w;   // this warp's four
+    const int64_t srow0 = int64_t(st) * kTile + 32 * part + 4 * w;
     const int32_t page = pos0 < first ? __ldg(p.tables + int64_t(r) * p.max_pages + (pos0 >> 8)) : -1;   // a tile lies in one page
     const bool page_ok = page >= 0 && page < p.num_pages;
     const uint8_t* pg = p.pool + int64_t(page_ok ? page : 0) * kPageBytes;
-    __half* dst0 = p.rows + (int64_t(kv * kHkv + h) * p.store_rows + int64_t(st) * kTile) * kD;
-    float* nrm0 = p.norms + int64_t(kv * kHkv + h) * p.store_rows + int64_t(st) * kTile;
-    const float unit = kv ? Sh::kPScale : 1.f;
+    __half* const k0 = p.rows + (int64_t(h) * p.store_rows + srow0) * kD;
+    __half* const v0 = p.rows + (int64_t(kHkv + h) * p.store_rows + srow0) * kD;
+    float size = 0.f;   // lane i < 4: that of value i
     bool bad_page = false;
-#pragma unroll 4
-    for (int i = w; i < kTile; i += kRgPrepThreads / 32) {
+    uint4 raw_k[4], raw_v[4];   // a chunk vector's eight elements a lane; a cached one's word in .x, its norm in .y
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       const int32_t pos = pos0 + i;
-      float norm = 0.f;
-      if (pos >= first && pos < T) {   // the chunk's own
-        float v[8];
-        norm = 0.0625f * unit * rg_rotate((kv ? p.v : p.k) + (int64_t(row0 + pos - first) * kHkv + h) * kD, sb, v);
-        rg_store_row<kExact>(dst0 + int64_t(i) * kD, kv_part, v);
-      } else {
-        const bool seen = pos < first && (pos >= lo || pos < p.n_sink);
-        uint4 hi = make_uint4(0, 0, 0, 0), lo4 = hi;
-        bad_page |= seen && !page_ok;
-        if (seen && page_ok) {
+      raw_k[i] = raw_v[i] = make_uint4(0, 0, 0, 0);
+      if (pos >= first && pos < T) {
+        const int64_t off = (int64_t(row0 + pos - first) * kHkv + h) * kD + lane * 8;
+        raw_k[i] = __ldg(reinterpret_cast<const uint4*>(p.k + off));
+        raw_v[i] = __ldg(reinterpret_cast<const uint4*>(p.v + off));
+      } else if (pos < first && (pos >= lo || pos < p.n_sink)) {
+        bad_page |= !page_ok;
+        if (page_ok) {
           const int slot = h * kPage + (pos & (kPage - 1));
-          const uint32_t word = __ldg(reinterpret_cast<const uint32_t*>(pg + (kv ? kVWords : kKWords) + int64_t(slot) * 128) + lane);
-          norm = ldg_half(pg + (kv ? kVNorms : kKNorms) + slot * 2) * unit;
-          hi = make_uint4(pair_s[word & 255u], pair_s[(word >> 8) & 255u], pair_s[(word >> 16) & 255u], pair_s[word >> 24]);
-          if constexpr (kExact)
-            lo4 = make_uint4(res_s[word & 255u], res_s[(word >> 8) & 255u], res_s[(word >> 16) & 255u], res_s[word >> 24]);
+          raw_k[i].x = ldg32(pg + kKWords + int64_t(slot) * 128 + lane * 4);
+          raw_v[i].x = ldg32(pg + kVWords + int64_t(slot) * 128 + lane * 4);
+          raw_k[i].y = __ldg(reinterpret_cast<const unsigned short*>(pg + kKNorms + slot * 2));
+          raw_v[i].y = __ldg(reinterpret_cast<const unsigned short*>(pg + kVNorms + slot * 2));
         }
-        *reinterpret_cast<uint4*>(dst0 + int64_t(i) * kD + lane * 8) = hi;
-        if constexpr (kExact) *reinterpret_cast<uint4*>(dst0 + kv_part + int64_t(i) * kD + lane * 8) = lo4;
-      }
-      if (lane == 0) nrm0[i] = norm;
+      }   // else nobody sees it: zeros
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int32_t pos = pos0 + i;
+      float mine;
+      if (pos >= first && pos < T) {   // the chunk's own
+        float a[8], b[8];
+        const uint32_t ktop = rg_rotate(raw_k[i], sb, a), vtop = rg_rotate(raw_v[i], sb, b);
+        const bool fits = ktop <= kRgTop && vtop <= kRgTop;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          a[x] = fits ? a[x] * 0.0625f : __uint_as_float(0x7FC00000u);
+          b[x] = fits ? b[x] : 0.f;
+        }
+        mine = 0.0625f * Sh::kPScale * rg_scale(fits ? vtop : 0u, b);
+        rg_store_row<kExact>(k0 + i * kD, kv_part, a);
+        rg_store_row<kExact>(v0 + i * kD, kv_part, b);
+      } else {
+        const float kn = __half2float(__ushort_as_half(uint16_t(raw_k[i].y))), vn = __half2float(__ushort_as_half(uint16_t(raw_v[i].y)));
+        const bool fits = fabsf(vn) <= 65504.f;   // false: an infinity or a NaN
+        const uint32_t wk = raw_k[i].x, wv = raw_v[i].x;
+        const int copy = lane & 7;
+        const __half2 n2 = fits ? __half2half2(__ushort_as_half(uint16_t(raw_k[i].y))) : __half2half2(__ushort_as_half(0x7E00));
+        uint32_t kk[4], vv[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t c = pair_s[(wk >> (8 * x)) & 255u][copy];
+          vv[x] = pair_s[(wv >> (8 * x)) & 255u][copy];
+          if constexpr (!kExact) {
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&c), n2);
+            kk[x] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+        }
+        if constexpr (kExact) {
+          float a[8];
+          uint32_t vl[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t ch = pair_s[(wk >> (8 * x)) & 255u][copy], cl = res_s[(wk >> (8 * x)) & 255u][copy];
+            const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&ch)), lf = __half22float2(*reinterpret_cast<const __half2*>(&cl));
+            const float n = fits ? kn : __uint_as_float(0x7FC00000u);
+            a[2 * x] = (hf.x + lf.x) * n;
+            a[2 * x + 1] = (hf.y + lf.y) * n;
+            vl[x] = res_s[(wv >> (8 * x)) & 255u][copy];
+          }
+          rg_store_row<true>(k0 + i * kD, kv_part, a);
+          *reinterpret_cast<uint4*>(v0 + kv_part + i * kD + lane * 8) = make_uint4(vl[0], vl[1], vl[2], vl[3]);
+        } else {
+          *reinterpret_cast<uint4*>(k0 + i * kD + lane * 8) = make_uint4(kk[0], kk[1], kk[2], kk[3]);
+        }
+        *reinterpret_cast<uint4*>(v0 + i * kD + lane * 8) = make_uint4(vv[0], vv[1], vv[2], vv[3]);
+        mine = fits ? vn * Sh::kPScale : 0.f;
+      }
+      if (lane == i) size = mine;
+    }
+    if (lane < 4) p.norms[int64_t(h) * p.store_rows + srow0 + lane] = size;
     if (bad_page && lane == 0) record_error(p.status, TQ4_ERR_PAGE_RANGE);
   }
 }
@@ -536,9 +596,43 @@ __device__ __forceinline__ void fwht32(float (&v)[32]) {
       }
 }
 
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pair_f32(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpair_f32(uint64_t d, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d)); }
+__device__ __forceinline__ uint64_t fma2_f32(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2_f32(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2_f32(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// the largest of three (a NaN is passed over)
+__device__ __forceinline__ float max3_f32(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+template <int N>
+__device__ __forceinline__ void rg_ld_scores(uint32_t taddr, uint32_t (&r)[N]) {
+  if constexpr (N == 64) tm_ld64(taddr, r);
+  else tm_ld32(taddr, r);
+}
+
 template <bool kExact>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
-    ragged_attend_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kvmap) {
+    ragged_attend_kernel(const __grid_constant__ RaggedParams p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kvmap) {
   using Sh = RgShape<kExact>;
   constexpr int kTile = Sh::kTile, kStages = Sh::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -613,12 +707,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
     RgSeg g;
     if (w < kRgSoftWarps) {
       // =========================================================== softmax / epilogue
-      const int r_local = 32 * w + lane;
-      const uint32_t lane_addr = tmem + (uint32_t(32 * w) << 16);
-      uint8_t* const stage = smem + w * 16384;   // this warp's 16 KiB of the Q panels, free once the item's last QK has run
-      const float* norms = reinterpret_cast<const float*>(smem + Sh::kNormOff);
+      constexpr int kC = kTile / 2;                 // columns of this thread
+      const int quad = w & 3, half = w >> 2;
+      const int r_local = 32 * quad + lane;
+      const uint32_t lane_addr = tmem + (uint32_t(32 * quad) << 16);
+      uint8_t* const stage = smem + w * 8192;       // this warp's 8 KiB of the Q panels, free once the item's last QK has run
+      const float* norms = reinterpret_cast<const float*>(smem + Sh::kNormOff) + kC * half;
+      float* const maxima = reinterpret_cast<float*>(smem + Sh::kMaxOff);
+      volatile uint32_t* const ok_s = reinterpret_cast<volatile uint32_t*>(smem + Sh::kOkOff);
       int t = 0;      // tiles of this pair so far
       bool ok = true;
+      // The two warps of these rows meet (their shared-memory writes before it are seen after it) and agree on
+      // going on, so that after a wait that gave up both leave at the same meeting.
+      auto both = [ok_s, quad, w, lane, &ok](int buf) {
+        if (lane == 0) ok_s[buf * kRgSoftWarps + w] = ok ? 1u : 0u;
+        asm volatile("bar.sync %0, 64;\n" ::"r"(quad + 1) : "memory");
+        ok = ok_s[buf * kRgSoftWarps + quad] != 0 && ok_s[buf * kRgSoftWarps + quad + 4] != 0;
+      };
       while (ok && walk.next(g)) {
         const RgReq rq = p.req[p.blk_req[g.blk]];
         const int rb = g.blk - rq.blk0;
@@ -628,50 +733,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         const int P = rq.first + (256 * rb + row) / 6;              // this row's position
         const float fac = p.qfac[int64_t(g.head) * kGroup * p.n_tok + int64_t(rq.row0) * kGroup + 256 * rb + row];
         float m_ref = -INFINITY, l_sum = 0.f;
+        bool left_early = false;
         for (int j = 0; j < g.n; ++j, ++t) {
           const int b = t & 1;
           const int at = g.tile + j;
-          const int pos0 = (at < span.sinks ? at : at + span.skip) * kTile;
-          if (!(ok = warp_wait(bar(kRgNFull + (t & 3)), (t >> 2) & 1))) break;
-          if (!(ok = warp_wait(bar(kRgSFull + b), (t >> 1) & 1))) break;
+          const int pos0 = (at < span.sinks ? at : at + span.skip) * kTile + kC * half;   // of this thread's columns
+          ok = ok && warp_wait(bar(kRgNFull + (t & 3)), (t >> 2) & 1) && warp_wait(bar(kRgSFull + b), (t >> 1) & 1);
           tc_fence_after();
-          const float4* kn4 = reinterpret_cast<const float4*>(norms + (t & 3) * 2 * kTile);
-          const float4* vn4 = kn4 + kTile / 4;
-          uint32_t sr[kTile / 64][64];
-          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          const bool full = __all_sync(0xffffffffu, pos0 + kTile - 1 <= P && (pos0 > P - p.window || pos0 + kTile <= p.n_sink));
+          uint32_t sr[kC];
+          float mx = -INFINITY;
+          if (ok) {
+            rg_ld_scores<kC>(lane_addr + 128 * b + kC * half, sr);
+            if (!__all_sync(0xffffffffu, pos0 + kC - 1 <= P && (pos0 > P - p.window || pos0 + kC <= p.n_sink))) {
 #pragma unroll
-          for (int c = 0; c < kTile / 64; ++c) {
-            tm_ld64(lane_addr + 128 * b + 64 * c, sr[c]);
-            if (full) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float4 k = kn4[16 * c + i];
-                const float kk[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float s = __uint_as_float(sr[c][4 * i + e]) * kk[e];
-                  sr[c][4 * i + e] = __float_as_uint(s);
-                  mx4[e] = fmaxf(mx4[e], s);
-                }
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float4 k = kn4[16 * c + i];
-                const float kk[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int pos = pos0 + 64 * c + 4 * i + e;
-                  const bool see = pos <= P && (pos > P - p.window || pos < p.n_sink);
-                  const float s = see ? __uint_as_float(sr[c][4 * i + e]) * kk[e] : -INFINITY;
-                  sr[c][4 * i + e] = __float_as_uint(s);
-                  mx4[e] = fmaxf(mx4[e], s);
-                }
+              for (int i = 0; i < kC; ++i) {
+                const int pos = pos0 + i;
+                if (!(pos <= P && (pos > P - p.window || pos < p.n_sink))) sr[i] = 0xFF800000u;   // -infinity
               }
             }
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < kC; i += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) m4[e] = max3_f32(m4[e], __uint_as_float(sr[i + e]), __uint_as_float(sr[i + 4 + e]));
+            mx = max3_f32(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
+            maxima[(2 * b + half) * kPfRows + r_local] = mx;
           }
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fac;   // in log2 units
+          both(b);   // (also: both have read their scores, so P may take their columns)
+          if ((left_early = !ok)) break;
+          mx = fmaxf(mx, maxima[(2 * b + (half ^ 1)) * kPfRows + r_local]) * fac;   // in log2 units
           const bool raise = mx > m_ref + Sh::kLazy;
           float alpha = 1.f;
           if (raise) {
@@ -680,51 +770,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
             l_sum *= alpha;
           }
           const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-          float l4[4] = {0.f, 0.f, 0.f, 0.f};
-          // P over the scores: 32 columns per 64 positions (fp32: hi, then lo)
+          const uint64_t fac2 = pair_f32(fac, fac), mu2 = pair_f32(-mu, -mu);
+          uint64_t l2[2] = {0ull, 0ull};
+          // P over the scores: a column per two positions (fp32: hi in the first half, lo in the second)
+          const float4* vn4 = reinterpret_cast<const float4*>(norms + (t & 3) * kTile);
+          uint32_t pk[kC / 2], pl[kExact ? kC / 2 : 1];
 #pragma unroll
-          for (int c = 0; c < kTile / 64; ++c) {
-            uint32_t pk[32];
+          for (int i = 0; i < kC / 4; ++i) {
+            const float4 v = vn4[i];
+            const uint64_t v2[2] = {pair_f32(v.x, v.y), pair_f32(v.z, v.w)};
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float4 v = vn4[16 * c + i];
-              const float vv[4] = {v.x, v.y, v.z, v.w};
-              float pw[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float s = __uint_as_float(sr[c][4 * i + e]);
-                const float pr = fast_exp2(fmaf(s, fac, -mu));   // +0 when masked
-                l4[e] += pr;
-                pw[e] = pr * vv[e];
-                if (!full) pw[e] = s == -INFINITY ? 0.f : pw[e];   // a masked position's norm may be anything
-                if constexpr (kExact) sr[c][4 * i + e] = __float_as_uint(pw[e]);
+            for (int e = 0; e < 2; ++e) {
+              const uint64_t x = fma2_f32(pair_f32(__uint_as_float(sr[4 * i + 2 * e]), __uint_as_float(sr[4 * i + 2 * e + 1])), fac2, mu2);
+              float x0, x1;
+              unpair_f32(x, x0, x1);
+              const uint64_t pr = pair_f32(fast_exp2(x0), fast_exp2(x1));   // +0 when masked
+              l2[e] = add2_f32(l2[e], pr);
+              unpair_f32(mul2_f32(pr, v2[e]), x0, x1);
+              pk[2 * i + e] = pack_half2(x0, x1);
+              if constexpr (kExact) {
+                const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&pk[2 * i + e]));
+                pl[2 * i + e] = pack_half2(x0 - hi.x, x1 - hi.y);
               }
-              pk[2 * i] = pack_half2(pw[0], pw[1]);
-              pk[2 * i + 1] = pack_half2(pw[2], pw[3]);
-            }
-            tm_st32(lane_addr + 128 * b + 32 * c, pk);
-            if constexpr (kExact) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&pk[i]));
-                pk[i] = pack_half2(__uint_as_float(sr[c][2 * i]) - hi.x, __uint_as_float(sr[c][2 * i + 1]) - hi.y);
-              }
-              tm_st32(lane_addr + 128 * b + 32, pk);
             }
           }
-          l_sum += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          float la, lb, lc, ld;
+          unpair_f32(l2[0], la, lb);
+          unpair_f32(l2[1], lc, ld);
+          l_sum += (la + lb) + (lc + ld);
+          if constexpr (kExact) {
+            tm_st16(lane_addr + 128 * b + 16 * half, pk);
+            tm_st16(lane_addr + 128 * b + 32 + 16 * half, pl);
+          } else {
+            tm_st32(lane_addr + 128 * b + 32 * half, pk);
+          }
           tm_wait_st();
-          if (j > 0) {   // PV(t - 1) has completed: O may be rescaled
-            if (!(ok = warp_wait(bar(kRgVEmpty + ((t - 1) & 1)), ((t - 1) >> 1) & 1))) break;
+          if (j > 0) {   // PV(t - 1) has completed: O may be rescaled, half of its columns by each warp
+            ok = warp_wait(bar(kRgVEmpty + ((t - 1) & 1)), ((t - 1) >> 1) & 1);
+            if (!ok) continue;   // to the next meeting
             tc_fence_after();
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
+              for (int c = 0; c < 4; ++c) {
                 uint32_t ov[32];
-                tm_ld32(lane_addr + kTmO + 32 * c, ov);
+                tm_ld32(lane_addr + kTmO + 128 * half + 32 * c, ov);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-                tm_st32(lane_addr + kTmO + 32 * c, ov);
+                tm_st32(lane_addr + kTmO + 128 * half + 32 * c, ov);
               }
               tm_wait_st();
             }
@@ -734,55 +826,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
           // (test hook: the first P signals are withheld, so the issuer's wait for them runs out)
           if (lane == 0 && !(p.test_withhold && t < 2)) mbar_arrive_cluster(lead_bar0 + 8u * uint32_t(kRgPFull + b));
         }
-        if (!ok) break;
+        if (left_early) break;
         // ---- the item's rows: wait for its last PV; R^T; out
-        if (!(ok = warp_wait(bar(kRgVEmpty + ((t - 1) & 1)), ((t - 1) >> 1) & 1))) break;
+        ok = ok && warp_wait(bar(kRgVEmpty + ((t - 1) & 1)), ((t - 1) >> 1) & 1);
         tc_fence_after();
+        // the two halves' sums, through the buffer that the item's last tile did not use (read before `both` above)
+        maxima[(2 * (t & 1) + half) * kPfRows + r_local] = l_sum;
+        both(t & 1);
+        if (!ok) break;
+        l_sum += maxima[(2 * (t & 1) + (half ^ 1)) * kPfRows + r_local];
         const bool whole = g.part < 0;
         const float inv = !whole ? 0.0625f / Sh::kPScale : l_sum == 0.f ? 0.f : (0.0625f / Sh::kPScale) / l_sum;
-        const int in_item = int(rank) * kPfRows + 32 * w;   // this warp's first row of the item
-        if (!whole) p.pml[int64_t(g.part) * 256 + in_item + lane] = make_float2(m_ref, l_sum);
-#pragma unroll
-        for (int hp = 0; hp < 2; ++hp) {   // dims 128 hp ..: the transform's top level is a sum or a difference
+        const int in_item = int(rank) * kPfRows + 32 * quad;   // this warp's first row of the item
+        if (!whole && half == 0) p.pml[int64_t(g.part) * 256 + in_item + lane] = make_float2(m_ref, l_sum);
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t a[32], d[32];
-            tm_ld32(lane_addr + kTmO + 32 * c, a);
-            tm_ld32(lane_addr + kTmO + 128 + 32 * c, d);
+        for (int sp = 0; sp < 2; ++sp) {   // dims 128 half + 64 sp ..: the transform's top two levels are signed sums
+          const float s7 = half ? -1.f : 1.f, s6 = sp ? -1.f : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
             float v[32];
+            uint32_t o[32];
+            tm_ld32(lane_addr + kTmO + 32 * c, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = hp ? __uint_as_float(a[i]) - __uint_as_float(d[i]) : __uint_as_float(a[i]) + __uint_as_float(d[i]);
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]);
+            tm_ld32(lane_addr + kTmO + 64 + 32 * c, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(s6, __uint_as_float(o[i]), v[i]);
+            tm_ld32(lane_addr + kTmO + 128 + 32 * c, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(s7, __uint_as_float(o[i]), v[i]);
+            tm_ld32(lane_addr + kTmO + 192 + 32 * c, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(s7 * s6, __uint_as_float(o[i]), v[i]);
             fwht32(v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)   // row `lane` of [32][128] floats, 16-byte chunks swizzled by the row
-              *reinterpret_cast<float4*>(stage + lane * 512 + (((8 * c + i) ^ lane) << 4)) =
+            for (int i = 0; i < 8; ++i)   // row `lane` of [32][64] floats, 16-byte chunks swizzled by the row
+              *reinterpret_cast<float4*>(stage + lane * 256 + (((8 * c + i) ^ (lane & 15)) << 4)) =
                   make_float4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
           }
           __syncwarp();
           const int li = lane & 15;
-#pragma unroll 2
-          for (int it = 0; it < 16; ++it) {   // two rows at a time: the two levels across the 32-dim chunks, signs, store
+          const uint32_t sg0 = p.signs.bits[4 * half + 2 * sp] >> (2 * li), sg1 = p.signs.bits[4 * half + 2 * sp + 1] >> (2 * li);
+#pragma unroll 4
+          for (int it = 0; it < 16; ++it) {   // two rows at a time: the level across the 32-dim chunks, signs, store
             const int rr = 2 * it + (lane >> 4);
-            float2 x[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              x[c] = *reinterpret_cast<const float2*>(stage + rr * 512 + (((8 * c + (li >> 1)) ^ rr) << 4) + (li & 1) * 8);
+            const uint8_t* src = stage + rr * 256 + (li & 1) * 8;
+            const float2 x0 = *reinterpret_cast<const float2*>(src + (((li >> 1) ^ (rr & 15)) << 4));
+            const float2 x1 = *reinterpret_cast<const float2*>(src + (((8 + (li >> 1)) ^ (rr & 15)) << 4));
             if (in_item + rr < n_rows) {
-              const float2 s0 = make_float2(x[0].x + x[1].x, x[0].y + x[1].y), d0 = make_float2(x[0].x - x[1].x, x[0].y - x[1].y);
-              const float2 s1 = make_float2(x[2].x + x[3].x, x[2].y + x[3].y), d1 = make_float2(x[2].x - x[3].x, x[2].y - x[3].y);
-              float2 y[4] = {make_float2(s0.x + s1.x, s0.y + s1.y), make_float2(d0.x + d1.x, d0.y + d1.y),
-                             make_float2(s0.x - s1.x, s0.y - s1.y), make_float2(d0.x - d1.x, d0.y - d1.y)};
+              const float2 y0 = make_float2(apply_sign(x0.x + x1.x, sg0, 0), apply_sign(x0.y + x1.y, sg0, 1));
+              const float2 y1 = make_float2(apply_sign(x0.x - x1.x, sg1, 0), apply_sign(x0.y - x1.y, sg1, 1));
               const int ir = 256 * rb + in_item + rr, tok = rq.row0 + ir / 6, jh = ir % 6;
-              const int64_t off = whole ? (int64_t(tok) * kHq + g.head * kGroup + jh) * kD : (int64_t(g.part) * 256 + in_item + rr) * kD;
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const uint32_t sw = p.signs.bits[4 * hp + c] >> (2 * li);
-                y[c].x = apply_sign(y[c].x, sw, 0);
-                y[c].y = apply_sign(y[c].y, sw, 1);
-                const int64_t o = off + 128 * hp + 32 * c + 2 * li;
-                if (!whole) *reinterpret_cast<float2*>(p.po + o) = y[c];
-                else if (kExact) *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o) = y[c];
-                else *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(p.out) + o) = __floats2bfloat162_rn(y[c].x, y[c].y);
+              const int64_t off = (whole ? (int64_t(tok) * kHq + g.head * kGroup + jh) * kD : (int64_t(g.part) * 256 + in_item + rr) * kD) +
+                                  128 * half + 64 * sp + 2 * li;
+              if (!whole || kExact) {
+                float* dst = (whole ? static_cast<float*>(p.out) : p.po) + off;
+                *reinterpret_cast<float2*>(dst) = y0;
+                *reinterpret_cast<float2*>(dst + 32) = y1;
+              } else {
+                uint16_t* dst = static_cast<uint16_t*>(p.out) + off;
+                *reinterpret_cast<__nv_bfloat162*>(dst) = __floats2bfloat162_rn(y0.x, y0.y);
+                *reinterpret_cast<__nv_bfloat162*>(dst + 32) = __floats2bfloat162_rn(y1.x, y1.y);
               }
             }
           }
@@ -831,11 +935,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
 #pragma unroll
                 for (int d = 0; d < 4; ++d) tma_load_2d(dst + d * Sh::kKPanel, &kvmap, 64 * d, int(row), fb);
               }
-              // norms: slot t & 3 was read by tile t - 4, whose PV came before the QK just waited for
-              const uint32_t nb = bar(kRgNFull + (t & 3)), nd = sbase + Sh::kNormOff + (t & 3) * 2 * kTile * 4;
-              mbar_expect_tx(nb, 2 * kTile * 4);
-              bulk_load(nd, p.norms + g.head * p.store_rows + srow, kTile * 4, nb);
-              bulk_load(nd + kTile * 4, p.norms + (kHkv + g.head) * p.store_rows + srow, kTile * 4, nb);
+              // the values' sizes: slot t & 3 was read by tile t - 4, whose PV came before the QK just waited for
+              const uint32_t nb = bar(kRgNFull + (t & 3));
+              mbar_expect_tx(nb, kTile * 4);
+              bulk_load(sbase + Sh::kNormOff + (t & 3) * kTile * 4, p.norms + g.head * p.store_rows + srow, kTile * 4, nb);
             }
           }
         }
@@ -1024,8 +1127,8 @@ inline cudaError_t ragged_set_attrs() {
 
 template <bool kExact>
 cudaError_t launch_ragged_t(RaggedParams& p, const CUtensorMap& qmap, const CUtensorMap& kvmap, const RgLayout& l, int num_sms, cudaStream_t st) {
-  // units of the prep: at most 8 per row tile and one per token
-  const int64_t units = l.store_rows / RgShape<kExact>::kTile * 8 + p.n_tok;
+  // units of the prep: one per 32 row positions and KV head, and one per token
+  const int64_t units = l.store_rows / 32 * kHkv + p.n_tok;
   const dim3 prep(unsigned(std::min<int64_t>(units, int64_t(num_sms) * 6) + 1));
   cudaError_t e = launch_pdl(ragged_prep_kernel<kExact>, prep, dim3(kRgPrepThreads), size_t(p.n_req) * 8, st, p);
   if (e != cudaSuccess) return e;

@@ -539,9 +539,10 @@ int tq4_decode_attention_window(tq4_ctx* ctx, const void* pool, int32_t num_page
  * A request whose rows or length are inconsistent (cu_tok out of order or past n_tok, a
  * length below its tokens or past the table) gets zeros where its rows are its own, and
  * TQ4_ERR_SEQ is recorded. bf16 results carry the operands as single f16 values (each
- * rounded once, relative 2^-11), fp32 results as hi + lo pairs. A chunk vector with an
- * infinity or a NaN makes the results of those who see it NaN, of no other. A rotated
- * value coordinate of 65,504 or more overflows, as its fp16 norm does in the cache. At most
+ * rounded once, relative 2^-11), fp32 results as hi + lo pairs. A vector with an infinity
+ * or a NaN (in the chunk also one with a rotated coordinate of 32,768 or more, which the
+ * cache's fp16 norm hardly holds either) makes the results of those who see it NaN, of no
+ * other. At most
  * TQ4_RAGGED_MAX_REQUESTS requests. The workspace holds one f16 row (fp32: two) per visible
  * position, KV head, K and V: 4 KiB (8 KiB) a position, for at most sinks + window + new
  * positions of each request. */
