@@ -66,8 +66,9 @@ struct RgShape {
   static constexpr uint32_t kVOff = kKOff + kStages * kParts * kKPart;
   static constexpr uint32_t kNormOff = kVOff + kStages * kParts * kVPart;   // [slots][kTile] f32: sizes of the values
   static constexpr uint32_t kMaxOff = kNormOff + kRgNormSlots * kTile * 4;   // [2][2 halves][128] f32: row maxima
-  static constexpr uint32_t kOkOff = kMaxOff + 2 * 2 * kPfRows * 4;          // [2][warps] u32: still at work
-  static constexpr uint32_t kBarOff = kOkOff + 2 * kRgSoftWarps * 4;
+  static constexpr uint32_t kSumOff = kMaxOff + 2 * 2 * kPfRows * 4;         // [2 halves][128] f32: row sums
+  static constexpr uint32_t kOkOff = kSumOff + 2 * kPfRows * 4;              // [3][warps] u32: still at work
+  static constexpr uint32_t kBarOff = kOkOff + 3 * kRgSoftWarps * 4 + 32;
   static constexpr uint32_t kMiscOff = kBarOff + 256;         // [0] TMEM base, [1] abort
   static constexpr uint32_t kSmem = kMiscOff + 64 + 1024;     // + alignment slack
   static constexpr float kLazy = kExact ? 0.f : 4.f;           // P = p n_v / 16 <= 2^4 * 65504 / 16; fp32: p <= 1, P = p n_v
@@ -77,7 +78,7 @@ static_assert(RgShape<false>::kSmem <= 227u * 1024u && RgShape<true>::kSmem <= 2
 
 // barriers (8 B each)
 constexpr int kRgQFull = 0, kRgQPeer = 1, kRgKFull = 2, kRgKPeer = 4, kRgVFull = 6, kRgVPeer = 8, kRgNFull = 10,
-              kRgPFull = 14, kRgSFull = 16, kRgVEmpty = 18, kRgEpi = 20, kRgDrain = 21;
+              kRgPFull = 14, kRgSFull = 16, kRgVEmpty = 18, kRgOFree = 20, kRgDrain = 21, kRgQFree = 22;
 
 struct RgReq {
   int32_t row0, n_new;   // rows of q, k, v; 0 new tokens for a request without work
@@ -123,7 +124,7 @@ struct RaggedParams {
   __half* rows;       // [parts][K, V][4][store_rows][256]
   float* norms;       // [4][store_rows] sizes of the values
   int64_t store_rows;
-  float* po;          // [2 max_pairs][256][256]
+  float* po;          // [2 max_pairs][dims / 4][256 rows][4]
   float2* pml;        // [2 max_pairs][256]
 };
 
@@ -519,7 +520,16 @@ __global__ void __launch_bounds__(kRgPrepThreads) ragged_prep_kernel(const Ragge
   }
 }
 
-// 64 consecutive TMEM columns of this thread's lane (load and wait in one statement, as tm_ld32)
+// 16 and 64 consecutive TMEM columns of this thread's lane (load and wait in one statement, as tm_ld32)
+__device__ __forceinline__ void tm_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tm_ld64(uint32_t taddr, uint32_t (&r)[64]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
@@ -596,6 +606,13 @@ __device__ __forceinline__ void fwht32(float (&v)[32]) {
       }
 }
 
+// One arrival on a barrier of the pair, at its default scope. What it orders lies in tensor memory
+// (ordered by the tcgen05 fences on both sides) or was written by a copy that has completed: no
+// generic-proxy store of this thread has to be seen by the other CTA. A release at cluster scope
+// costs 900 cycles here, an acquire 400 (measured with clock64), a tile's products 2,048.
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
+}
 // two fp32 operations in one instruction
 __device__ __forceinline__ uint64_t pair_f32(float a, float b) {
   uint64_t d;
@@ -659,8 +676,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
       mbar_init(bar(kRgVEmpty + b), 1);
     }
     for (int b = 0; b < kRgNormSlots; ++b) mbar_init(bar(kRgNFull + b), 1);
-    mbar_init(bar(kRgEpi), kRgSoftWarps);
+    mbar_init(bar(kRgOFree), 2 * kRgSoftWarps);
     mbar_init(bar(kRgDrain), 1);
+    mbar_init(bar(kRgQFree), 1);
     misc[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -682,7 +700,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
   const uint32_t peer_abort = map_to_rank(sbase + Sh::kMiscOff + 4, rank ^ 1u);
   auto bounded_wait = [misc, spin_limit, status, peer_abort](uint32_t b, uint32_t parity) -> bool {
     uint32_t spins = 0;
-    while (!mbar_try_wait_cluster(b, parity)) {
+    while (!mbar_try_wait(b, parity)) {
       if (misc[1]) return false;
       if (++spins > spin_limit) {
         misc[1] = 1;
@@ -698,7 +716,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
   };
   // copies that an aborted call may have in flight end before the CTA does
   auto drain = [](uint32_t b, uint32_t parity) {
-    for (uint32_t spins = 0; !mbar_try_wait_cluster(b, parity) && spins < TQ4_DEFAULT_WAIT_POLLS; ++spins) {
+    for (uint32_t spins = 0; !mbar_try_wait(b, parity) && spins < TQ4_DEFAULT_WAIT_POLLS; ++spins) {
     }
   };
 
@@ -711,9 +729,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
       const int quad = w & 3, half = w >> 2;
       const int r_local = 32 * quad + lane;
       const uint32_t lane_addr = tmem + (uint32_t(32 * quad) << 16);
-      uint8_t* const stage = smem + w * 8192;       // this warp's 8 KiB of the Q panels, free once the item's last QK has run
       const float* norms = reinterpret_cast<const float*>(smem + Sh::kNormOff) + kC * half;
       float* const maxima = reinterpret_cast<float*>(smem + Sh::kMaxOff);
+      float* const sums = reinterpret_cast<float*>(smem + Sh::kSumOff);
       volatile uint32_t* const ok_s = reinterpret_cast<volatile uint32_t*>(smem + Sh::kOkOff);
       int t = 0;      // tiles of this pair so far
       bool ok = true;
@@ -824,78 +842,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
           tc_fence_before();
           __syncwarp();
           // (test hook: the first P signals are withheld, so the issuer's wait for them runs out)
-          if (lane == 0 && !(p.test_withhold && t < 2)) mbar_arrive_cluster(lead_bar0 + 8u * uint32_t(kRgPFull + b));
+          if (lane == 0 && !(p.test_withhold && t < 2)) mbar_arrive_peer(lead_bar0 + 8u * uint32_t(kRgPFull + b));
         }
         if (left_early) break;
         // ---- the item's rows: wait for its last PV; R^T; out
         ok = ok && warp_wait(bar(kRgVEmpty + ((t - 1) & 1)), ((t - 1) >> 1) & 1);
         tc_fence_after();
-        // the two halves' sums, through the buffer that the item's last tile did not use (read before `both` above)
-        maxima[(2 * (t & 1) + half) * kPfRows + r_local] = l_sum;
-        both(t & 1);
+        sums[half * kPfRows + r_local] = l_sum;
+        both(2);
         if (!ok) break;
-        l_sum += maxima[(2 * (t & 1) + (half ^ 1)) * kPfRows + r_local];
+        l_sum += sums[(half ^ 1) * kPfRows + r_local];
         const bool whole = g.part < 0;
         const float inv = !whole ? 0.0625f / Sh::kPScale : l_sum == 0.f ? 0.f : (0.0625f / Sh::kPScale) / l_sum;
-        const int in_item = int(rank) * kPfRows + 32 * quad;   // this warp's first row of the item
-        if (!whole && half == 0) p.pml[int64_t(g.part) * 256 + in_item + lane] = make_float2(m_ref, l_sum);
+        const int in_item = int(rank) * kPfRows + r_local;     // this thread's row of the item
+        if (!whole && half == 0) p.pml[int64_t(g.part) * 256 + in_item] = make_float2(m_ref, l_sum);
+        const int ir = 256 * rb + in_item, tok = rq.row0 + ir / 6, jh = ir % 6;
+        const int64_t off = (int64_t(tok) * kHq + g.head * kGroup + jh) * kD + 128 * half;
+        const float s7 = half ? -1.f : 1.f;
 #pragma unroll 1
         for (int sp = 0; sp < 2; ++sp) {   // dims 128 half + 64 sp ..: the transform's top two levels are signed sums
-          const float s7 = half ? -1.f : 1.f, s6 = sp ? -1.f : 1.f;
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            float v[32];
-            uint32_t o[32];
-            tm_ld32(lane_addr + kTmO + 32 * c, o);
+          const float s6 = sp ? -1.f : 1.f, s76 = s7 * s6;
+          float v[2][32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]);
-            tm_ld32(lane_addr + kTmO + 64 + 32 * c, o);
+          for (int c = 0; c < 4; ++c) {   // 16 dims at a time
+            uint32_t o[16];
+            float* const x = v[c >> 1] + 16 * (c & 1);
+            tm_ld16(lane_addr + kTmO + 16 * c, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = fmaf(s6, __uint_as_float(o[i]), v[i]);
-            tm_ld32(lane_addr + kTmO + 128 + 32 * c, o);
+            for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(o[i]);
+            tm_ld16(lane_addr + kTmO + 64 + 16 * c, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = fmaf(s7, __uint_as_float(o[i]), v[i]);
-            tm_ld32(lane_addr + kTmO + 192 + 32 * c, o);
+            for (int i = 0; i < 16; ++i) x[i] = fmaf(s6, __uint_as_float(o[i]), x[i]);
+            tm_ld16(lane_addr + kTmO + 128 + 16 * c, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = fmaf(s7 * s6, __uint_as_float(o[i]), v[i]);
-            fwht32(v);
+            for (int i = 0; i < 16; ++i) x[i] = fmaf(s7, __uint_as_float(o[i]), x[i]);
+            tm_ld16(lane_addr + kTmO + 192 + 16 * c, o);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)   // row `lane` of [32][64] floats, 16-byte chunks swizzled by the row
-              *reinterpret_cast<float4*>(stage + lane * 256 + (((8 * c + i) ^ (lane & 15)) << 4)) =
-                  make_float4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+            for (int i = 0; i < 16; ++i) x[i] = fmaf(s76, __uint_as_float(o[i]), x[i]);
           }
-          __syncwarp();
-          const int li = lane & 15;
-          const uint32_t sg0 = p.signs.bits[4 * half + 2 * sp] >> (2 * li), sg1 = p.signs.bits[4 * half + 2 * sp + 1] >> (2 * li);
-#pragma unroll 4
-          for (int it = 0; it < 16; ++it) {   // two rows at a time: the level across the 32-dim chunks, signs, store
-            const int rr = 2 * it + (lane >> 4);
-            const uint8_t* src = stage + rr * 256 + (li & 1) * 8;
-            const float2 x0 = *reinterpret_cast<const float2*>(src + (((li >> 1) ^ (rr & 15)) << 4));
-            const float2 x1 = *reinterpret_cast<const float2*>(src + (((8 + (li >> 1)) ^ (rr & 15)) << 4));
-            if (in_item + rr < n_rows) {
-              const float2 y0 = make_float2(apply_sign(x0.x + x1.x, sg0, 0), apply_sign(x0.y + x1.y, sg0, 1));
-              const float2 y1 = make_float2(apply_sign(x0.x - x1.x, sg1, 0), apply_sign(x0.y - x1.y, sg1, 1));
-              const int ir = 256 * rb + in_item + rr, tok = rq.row0 + ir / 6, jh = ir % 6;
-              const int64_t off = (whole ? (int64_t(tok) * kHq + g.head * kGroup + jh) * kD : (int64_t(g.part) * 256 + in_item + rr) * kD) +
-                                  128 * half + 64 * sp + 2 * li;
-              if (!whole || kExact) {
-                float* dst = (whole ? static_cast<float*>(p.out) : p.po) + off;
-                *reinterpret_cast<float2*>(dst) = y0;
-                *reinterpret_cast<float2*>(dst + 32) = y1;
+          if (sp == 1) {   // O has been read: the next item's first PV may replace it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_peer(lead_bar0 + 8u * uint32_t(kRgOFree));
+          }
+          fwht32(v[0]);
+          fwht32(v[1]);
+          const uint32_t sg0 = p.signs.bits[4 * half + 2 * sp], sg1 = p.signs.bits[4 * half + 2 * sp + 1];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float a = v[0][i] * inv, d = v[1][i] * inv;
+            v[0][i] = apply_sign(a + d, sg0, i);
+            v[1][i] = apply_sign(a - d, sg1, i);
+          }
+          // a thread writes its own row, 64 dims in a piece: whole sectors, and no staging that the next item's
+          // queries would have to wait for
+          if (!whole) {   // [part][dims / 4][row]: the lanes' pieces lie side by side
+            float4* dst = reinterpret_cast<float4*>(p.po) + (int64_t(g.part) * 64 + 32 * half + 16 * sp) * 256 + in_item;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) dst[(8 * c + i) * 256] = make_float4(v[c][4 * i], v[c][4 * i + 1], v[c][4 * i + 2], v[c][4 * i + 3]);
+          } else if (in_item < n_rows) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if constexpr (kExact) {
+                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + off + 64 * sp + 32 * c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[c][4 * i], v[c][4 * i + 1], v[c][4 * i + 2], v[c][4 * i + 3]);
               } else {
-                uint16_t* dst = static_cast<uint16_t*>(p.out) + off;
-                *reinterpret_cast<__nv_bfloat162*>(dst) = __floats2bfloat162_rn(y0.x, y0.y);
-                *reinterpret_cast<__nv_bfloat162*>(dst + 32) = __floats2bfloat162_rn(y1.x, y1.y);
+                uint16_t* dst = static_cast<uint16_t*>(p.out) + off + 64 * sp + 32 * c;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) store8_bf16(dst + 8 * i, &v[c][8 * i]);
               }
             }
           }
-          __syncwarp();
         }
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");   // the next Q rows replace what was staged
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_local(bar(kRgEpi));
       }
     } else if (w == kRgKWarp || w == kRgVWarp) {
       // =========================================================== K tiles and norms; V tiles
@@ -955,7 +976,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         while (walk.next(g)) {
           const RgReq rq = p.req[p.blk_req[g.blk]];
           const int64_t row = int64_t(g.head) * kGroup * p.n_tok + int64_t(rq.row0) * kGroup + 256 * (g.blk - rq.blk0) + int(rank) * kPfRows;
-          if (s > 0 && !bounded_wait(bar(kRgEpi), (s - 1) & 1)) break;   // the last item's rows are out
+          if (s > 0 && !bounded_wait(bar(kRgQFree), (s - 1) & 1)) break;   // the last item's last QK has run
           mbar_expect_tx(bar(kRgQFull), Sh::kParts * Sh::kQPart);
 #pragma unroll
           for (int x = 0; x < Sh::kParts; ++x)
@@ -973,18 +994,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         bool ok = true;
         while (ok && walk.next(g)) {
           if (!(ok = bounded_wait(bar(kRgQFull), s & 1))) break;
-          mbar_arrive_cluster(lead_bar0 + 8u * uint32_t(kRgQPeer));
+          mbar_arrive_peer(lead_bar0 + 8u * uint32_t(kRgQPeer));
           ++s;
           for (int j = 0; ok && j <= g.n; ++j) {   // in the order in which rank 0 waits for them
             if (j < g.n) {
               const int u = t + j, st = u % kStages;
               if (!(ok = bounded_wait(bar(kRgKFull + st), (u / kStages) & 1))) break;
-              mbar_arrive_cluster(lead_bar0 + 8u * uint32_t(kRgKPeer + st));
+              mbar_arrive_peer(lead_bar0 + 8u * uint32_t(kRgKPeer + st));
             }
             if (j > 0) {
               const int u = t + j - 1, st = u % kStages;
               if (!(ok = bounded_wait(bar(kRgVFull + st), (u / kStages) & 1))) break;
-              mbar_arrive_cluster(lead_bar0 + 8u * uint32_t(kRgVPeer + st));
+              mbar_arrive_peer(lead_bar0 + 8u * uint32_t(kRgVPeer + st));
             }
           }
           t += g.n;
@@ -1018,12 +1039,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
                              idesc_qk, (x > 0 || kk > 0) ? 1u : 0u);
               }
               tc2_commit_both(bar(kRgSFull + (u & 1)));
+              if (j == g.n - 1) tc2_commit_both(bar(kRgQFree));
             }
             if (j > 0) {   // O += P V of tile j - 1
               const int u = t + j - 1, st = u % kStages;
               const uint32_t par = (u / kStages) & 1;
               if (!(ok = bounded_wait(bar(kRgVFull + st), par) && bounded_wait(bar(kRgVPeer + st), par) &&
-                         bounded_wait(bar(kRgPFull + (u & 1)), (u >> 1) & 1)))
+                         bounded_wait(bar(kRgPFull + (u & 1)), (u >> 1) & 1) &&
+                         (j > 1 || s < 2 || bounded_wait(bar(kRgOFree), s & 1))))   // the last item's rows have been read
                 break;
               tc_fence_after();
               const uint32_t p_t = tmem + 128 * (u & 1);
@@ -1056,13 +1079,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
 
 // --------------------------------------------------------------------------
 // combine: the rows of items that several pairs share. CTA (b, y) looks at the border before
-// pair b + 1's share: where it is the first border inside an item, rows 32 y .. of that item
-// are merged, o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
+// pair b + 1's share: where it is the first border inside an item, dims 16 y .. of that item's
+// rows are merged, one row a thread, o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
 // --------------------------------------------------------------------------
 template <bool kExact>
 __global__ void __launch_bounds__(256) ragged_combine_kernel(const RaggedParams p) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int b = int(blockIdx.x) + 1;
+  const int b = int(blockIdx.x) + 1, row = threadIdx.x;
   pdl_wait();
   pdl_launch_dependents();
   const int n_pairs = p.head->n_pairs;
@@ -1071,44 +1093,48 @@ __global__ void __launch_bounds__(256) ragged_combine_kernel(const RaggedParams 
   if (me.tile == 0) return;                                                        // no item is cut here
   if (prev.head == me.head && prev.blk == me.blk && prev.tile > 0) return;         // not its first cut
   const int part0 = 2 * (b - 1) + (prev.head == me.head && prev.blk == me.blk ? 0 : 1);
-  int last = b;   // pairs b .. last hold the rest of the item, as their first stretch
-  while (last + 1 < n_pairs) {
-    const RgStart s = p.starts[last + 1];
-    if (s.head != me.head || s.blk != me.blk) break;   // (its tile is then past 0)
-    ++last;
-  }
   const RgReq rq = p.req[p.blk_req[me.blk]];
   const int rb = me.blk - rq.blk0, n_rows = min(256, 6 * rq.n_new - 256 * rb);
-#pragma unroll 1
-  for (int x = 0; x < 4; ++x) {
-    const int row = 32 * int(blockIdx.y) + 8 * x + w;
-    if (row >= n_rows) break;
-    float M = p.pml[int64_t(part0) * 256 + row].x;
-    for (int i = b; i <= last; ++i) M = fmaxf(M, p.pml[int64_t(2 * i) * 256 + row].x);
-    float L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int i = b - 1; i <= last; ++i) {
-      const int64_t rec = int64_t(i < b ? part0 : 2 * i) * 256 + row;
-      const float2 ml = p.pml[rec];
-      if (ml.x == -INFINITY && ml.y == 0.f) continue;   // that stretch showed this row nothing
-      const float f = fast_exp2(ml.x - M);
-      L = fmaf(f, ml.y, L);
-      const float4* src = reinterpret_cast<const float4*>(p.po + rec * kD + lane * 8);
-      const float4 a = src[0], c = src[1];
-      o[0] = fmaf(f, a.x, o[0]); o[1] = fmaf(f, a.y, o[1]); o[2] = fmaf(f, a.z, o[2]); o[3] = fmaf(f, a.w, o[3]);
-      o[4] = fmaf(f, c.x, o[4]); o[5] = fmaf(f, c.y, o[5]); o[6] = fmaf(f, c.z, o[6]); o[7] = fmaf(f, c.w, o[7]);
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+  if (row >= n_rows) return;
+  // pairs b, b + 1, ... hold the rest of the item, as their first stretch, while their shares begin inside it
+  auto more = [&](int i) {
+    if (i >= n_pairs) return false;
+    const RgStart s = p.starts[i];
+    return s.head == me.head && s.blk == me.blk;
+  };
+  float M = p.pml[int64_t(part0) * 256 + row].x;
+  for (int i = b; more(i); ++i) M = fmaxf(M, p.pml[int64_t(2 * i) * 256 + row].x);
+  float L = 0.f, o[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] *= inv;
-    const int ir = 256 * rb + row;
-    const int64_t off = (int64_t(rq.row0 + ir / 6) * kHq + me.head * kGroup + ir % 6) * kD + lane * 8;
-    if constexpr (kExact) {
-      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + off);
-      dst[0] = make_float4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_float4(o[4], o[5], o[6], o[7]);
-    } else {
-      store8_bf16(static_cast<uint16_t*>(p.out) + off, o);
+  for (int x = 0; x < 16; ++x) o[x] = 0.f;
+  for (int i = b - 1; i < b || more(i); ++i) {
+    const int64_t part = i < b ? part0 : 2 * i;
+    const float2 ml = p.pml[part * 256 + row];
+    if (ml.x == -INFINITY && ml.y == 0.f) continue;   // that stretch showed this row nothing
+    const float f = fast_exp2(ml.x - M);
+    L = fmaf(f, ml.y, L);
+    const float4* src = reinterpret_cast<const float4*>(p.po) + (part * 64 + 4 * int(blockIdx.y)) * 256 + row;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float4 a = src[x * 256];
+      o[4 * x] = fmaf(f, a.x, o[4 * x]);
+      o[4 * x + 1] = fmaf(f, a.y, o[4 * x + 1]);
+      o[4 * x + 2] = fmaf(f, a.z, o[4 * x + 2]);
+      o[4 * x + 3] = fmaf(f, a.w, o[4 * x + 3]);
     }
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+  for (int x = 0; x < 16; ++x) o[x] *= inv;
+  const int ir = 256 * rb + row;
+  const int64_t off = (int64_t(rq.row0 + ir / 6) * kHq + me.head * kGroup + ir % 6) * kD + 16 * int(blockIdx.y);
+  if constexpr (kExact) {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + off);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+  } else {
+    store8_bf16(static_cast<uint16_t*>(p.out) + off, o);
+    store8_bf16(static_cast<uint16_t*>(p.out) + off + 8, o + 8);
   }
 }
 
@@ -1134,7 +1160,7 @@ cudaError_t launch_ragged_t(RaggedParams& p, const CUtensorMap& qmap, const CUte
   if (e != cudaSuccess) return e;
   e = launch_pdl(ragged_attend_kernel<kExact>, dim3(unsigned(2 * p.max_pairs)), dim3(kRgThreads), size_t(RgShape<kExact>::kSmem), st, p, qmap, kvmap);
   if (e != cudaSuccess || p.max_pairs < 2) return e;
-  return launch_pdl(ragged_combine_kernel<kExact>, dim3(unsigned(p.max_pairs - 1), 8), dim3(256), 0, st, p);
+  return launch_pdl(ragged_combine_kernel<kExact>, dim3(unsigned(p.max_pairs - 1), kD / 16), dim3(256), 0, st, p);
 }
 
 }  // namespace tq4
