@@ -67,8 +67,8 @@ struct RgShape {
   static constexpr uint32_t kNormOff = kVOff + kStages * kParts * kVPart;   // [slots][kTile] f32: sizes of the values
   static constexpr uint32_t kMaxOff = kNormOff + kRgNormSlots * kTile * 4;   // [2][2 halves][128] f32: row maxima
   static constexpr uint32_t kSumOff = kMaxOff + 2 * 2 * kPfRows * 4;         // [2 halves][128] f32: row sums
-  static constexpr uint32_t kOkOff = kSumOff + 2 * kPfRows * 4;              // [3][warps] u32: still at work
-  static constexpr uint32_t kBarOff = kOkOff + 3 * kRgSoftWarps * 4 + 32;
+  static constexpr uint32_t kSignOff = kSumOff + 2 * kPfRows * 4;            // [256] f32: the rotation's signs
+  static constexpr uint32_t kBarOff = kSignOff + kD * 4;
   static constexpr uint32_t kMiscOff = kBarOff + 256;         // [0] TMEM base, [1] abort
   static constexpr uint32_t kSmem = kMiscOff + 64 + 1024;     // + alignment slack
   static constexpr float kLazy = kExact ? 0.f : 4.f;           // P = p n_v / 16 <= 2^4 * 65504 / 16; fp32: p <= 1, P = p n_v
@@ -593,19 +593,15 @@ struct RgWalk {
   }
 };
 
-// 32-point Walsh-Hadamard transform in registers
-__device__ __forceinline__ void fwht32(float (&v)[32]) {
-#pragma unroll
-  for (int s = 1; s < 32; s <<= 1)
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if ((i & s) == 0) {
-        const float a = v[i], b = v[i + s];
-        v[i] = a + b;
-        v[i + s] = a - b;
-      }
+// one look at a barrier's phase
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(done)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return done != 0;
 }
-
 // One arrival on a barrier of the pair, at its default scope. What it orders lies in tensor memory
 // (ordered by the tcgen05 fences on both sides) or was written by a copy that has completed: no
 // generic-proxy store of this thread has to be seen by the other CTA. A release at cluster scope
@@ -635,12 +631,32 @@ __device__ __forceinline__ uint64_t add2_f32(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// 32-point Walsh-Hadamard transform in registers, element 2 i + k in half k of pair i
+__device__ __forceinline__ void fwht32(uint64_t (&v)[16]) {
+  const uint64_t minus = pair_f32(-1.f, -1.f);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float a, b;
+    unpair_f32(v[i], a, b);
+    v[i] = pair_f32(a + b, a - b);
+  }
+#pragma unroll
+  for (int s = 1; s < 16; s <<= 1)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if ((i & s) == 0) {
+        const uint64_t a = v[i], b = v[i + s];
+        v[i] = add2_f32(a, b);
+        v[i + s] = fma2_f32(b, minus, a);
+      }
+}
 // the largest of three (a NaN is passed over)
 __device__ __forceinline__ float max3_f32(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+constexpr uint32_t kRgGone = 0x7FC0DEADu;   // a NaN that no arithmetic gives
 template <int N>
 __device__ __forceinline__ void rg_ld_scores(uint32_t taddr, uint32_t (&r)[N]) {
   if constexpr (N == 64) tm_ld64(taddr, r);
@@ -682,6 +698,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
     misc[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
+  for (int i = tid; i < kD; i += kRgThreads)
+    reinterpret_cast<float*>(smem + Sh::kSignOff)[i] = sign_of(p.signs, i);
   if (w == 0) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(sbase + Sh::kMiscOff)
                  : "memory");
@@ -730,17 +748,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
       const int r_local = 32 * quad + lane;
       const uint32_t lane_addr = tmem + (uint32_t(32 * quad) << 16);
       const float* norms = reinterpret_cast<const float*>(smem + Sh::kNormOff) + kC * half;
-      float* const maxima = reinterpret_cast<float*>(smem + Sh::kMaxOff);
-      float* const sums = reinterpret_cast<float*>(smem + Sh::kSumOff);
-      volatile uint32_t* const ok_s = reinterpret_cast<volatile uint32_t*>(smem + Sh::kOkOff);
       int t = 0;      // tiles of this pair so far
       bool ok = true;
-      // The two warps of these rows meet (their shared-memory writes before it are seen after it) and agree on
-      // going on, so that after a wait that gave up both leave at the same meeting.
-      auto both = [ok_s, quad, w, lane, &ok](int buf) {
-        if (lane == 0) ok_s[buf * kRgSoftWarps + w] = ok ? 1u : 0u;
+      // The two warps of these rows swap a value per row through buf and agree on going on, so that after a wait
+      // that gave up both leave at the same meeting (the value is then kRgGone).
+      auto swap = [quad, half, r_local, &ok](float* buf, float mine) -> float {
+        buf[half * kPfRows + r_local] = ok ? mine : __uint_as_float(kRgGone);
         asm volatile("bar.sync %0, 64;\n" ::"r"(quad + 1) : "memory");
-        ok = ok_s[buf * kRgSoftWarps + quad] != 0 && ok_s[buf * kRgSoftWarps + quad + 4] != 0;
+        const float other = buf[(half ^ 1) * kPfRows + r_local];
+        ok = ok && __float_as_uint(other) != kRgGone;
+        return other;
       };
       while (ok && walk.next(g)) {
         const RgReq rq = p.req[p.blk_req[g.blk]];
@@ -775,11 +792,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
 #pragma unroll
               for (int e = 0; e < 4; ++e) m4[e] = max3_f32(m4[e], __uint_as_float(sr[i + e]), __uint_as_float(sr[i + 4 + e]));
             mx = max3_f32(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
-            maxima[(2 * b + half) * kPfRows + r_local] = mx;
           }
-          both(b);   // (also: both have read their scores, so P may take their columns)
+          // (also: both have read their scores, so P may take their columns)
+          const float other = swap(reinterpret_cast<float*>(smem + Sh::kMaxOff) + 2 * b * kPfRows, mx);
           if ((left_early = !ok)) break;
-          mx = fmaxf(mx, maxima[(2 * b + (half ^ 1)) * kPfRows + r_local]) * fac;   // in log2 units
+          mx = fmaxf(mx, other) * fac;   // in log2 units
           const bool raise = mx > m_ref + Sh::kLazy;
           float alpha = 1.f;
           if (raise) {
@@ -823,21 +840,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
             tm_st32(lane_addr + 128 * b + 32 * half, pk);
           }
           tm_wait_st();
-          if (j > 0) {   // PV(t - 1) has completed: O may be rescaled, half of its columns by each warp
+          // A raised reference rescales O, half of its columns by each warp, once PV(t - 1) has completed. (S(t) came
+          // after PV(t - 2), so the barrier's phase before this one is over and its parity names one phase only.)
+          if (j > 0 && __any_sync(0xffffffffu, raise)) {
             ok = warp_wait(bar(kRgVEmpty + ((t - 1) & 1)), ((t - 1) >> 1) & 1);
             if (!ok) continue;   // to the next meeting
             tc_fence_after();
-            if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                uint32_t ov[32];
-                tm_ld32(lane_addr + kTmO + 128 * half + 32 * c, ov);
+            for (int c = 0; c < 4; ++c) {
+              uint32_t ov[32];
+              tm_ld32(lane_addr + kTmO + 128 * half + 32 * c, ov);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-                tm_st32(lane_addr + kTmO + 128 * half + 32 * c, ov);
-              }
-              tm_wait_st();
+              for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+              tm_st32(lane_addr + kTmO + 128 * half + 32 * c, ov);
             }
+            tm_wait_st();
           }
           tc_fence_before();
           __syncwarp();
@@ -848,37 +865,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         // ---- the item's rows: wait for its last PV; R^T; out
         ok = ok && warp_wait(bar(kRgVEmpty + ((t - 1) & 1)), ((t - 1) >> 1) & 1);
         tc_fence_after();
-        sums[half * kPfRows + r_local] = l_sum;
-        both(2);
+        const float rest = swap(reinterpret_cast<float*>(smem + Sh::kSumOff), l_sum);
         if (!ok) break;
-        l_sum += sums[(half ^ 1) * kPfRows + r_local];
+        l_sum += rest;
         const bool whole = g.part < 0;
         const float inv = !whole ? 0.0625f / Sh::kPScale : l_sum == 0.f ? 0.f : (0.0625f / Sh::kPScale) / l_sum;
         const int in_item = int(rank) * kPfRows + r_local;     // this thread's row of the item
         if (!whole && half == 0) p.pml[int64_t(g.part) * 256 + in_item] = make_float2(m_ref, l_sum);
         const int ir = 256 * rb + in_item, tok = rq.row0 + ir / 6, jh = ir % 6;
         const int64_t off = (int64_t(tok) * kHq + g.head * kGroup + jh) * kD + 128 * half;
-        const float s7 = half ? -1.f : 1.f;
+        const float i7 = half ? -inv : inv;
+        const float4* const sgn4 = reinterpret_cast<const float4*>(smem + Sh::kSignOff) + 32 * half;
 #pragma unroll 1
         for (int sp = 0; sp < 2; ++sp) {   // dims 128 half + 64 sp ..: the transform's top two levels are signed sums
-          const float s6 = sp ? -1.f : 1.f, s76 = s7 * s6;
-          float v[2][32];
+          const float i6 = sp ? -inv : inv, i76 = sp ? -i7 : i7;
+          const uint64_t f[4] = {pair_f32(inv, inv), pair_f32(i6, i6), pair_f32(i7, i7), pair_f32(i76, i76)};
+          uint64_t v[2][16];   // pairs of dims 2 i, 2 i + 1 of each block of 32
 #pragma unroll
           for (int c = 0; c < 4; ++c) {   // 16 dims at a time
-            uint32_t o[16];
-            float* const x = v[c >> 1] + 16 * (c & 1);
-            tm_ld16(lane_addr + kTmO + 16 * c, o);
+            uint64_t* const x = v[c >> 1] + 8 * (c & 1);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(o[i]);
-            tm_ld16(lane_addr + kTmO + 64 + 16 * c, o);
+            for (int k = 0; k < 4; ++k) {
+              uint32_t o[16];
+              tm_ld16(lane_addr + kTmO + 64 * k + 16 * c, o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = fmaf(s6, __uint_as_float(o[i]), x[i]);
-            tm_ld16(lane_addr + kTmO + 128 + 16 * c, o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = fmaf(s7, __uint_as_float(o[i]), x[i]);
-            tm_ld16(lane_addr + kTmO + 192 + 16 * c, o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = fmaf(s76, __uint_as_float(o[i]), x[i]);
+              for (int i = 0; i < 8; ++i) {
+                const uint64_t y = pair_f32(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+                x[i] = k == 0 ? mul2_f32(y, f[0]) : fma2_f32(y, f[k], x[i]);
+              }
+            }
           }
           if (sp == 1) {   // O has been read: the next item's first PV may replace it
             tc_fence_before();
@@ -887,12 +902,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
           }
           fwht32(v[0]);
           fwht32(v[1]);
-          const uint32_t sg0 = p.signs.bits[4 * half + 2 * sp], sg1 = p.signs.bits[4 * half + 2 * sp + 1];
+          const uint64_t minus = pair_f32(-1.f, -1.f);
+          float y[2][32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float a = v[0][i] * inv, d = v[1][i] * inv;
-            v[0][i] = apply_sign(a + d, sg0, i);
-            v[1][i] = apply_sign(a - d, sg1, i);
+          for (int i = 0; i < 16; i += 2) {   // the level across the two blocks, and the signs
+            const float4 s0 = sgn4[16 * sp + i / 2], s1 = sgn4[16 * sp + 8 + i / 2];
+            const uint64_t m0[2] = {pair_f32(s0.x, s0.y), pair_f32(s0.z, s0.w)}, m1[2] = {pair_f32(s1.x, s1.y), pair_f32(s1.z, s1.w)};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              unpair_f32(mul2_f32(add2_f32(v[0][i + e], v[1][i + e]), m0[e]), y[0][2 * (i + e)], y[0][2 * (i + e) + 1]);
+              unpair_f32(mul2_f32(fma2_f32(v[1][i + e], minus, v[0][i + e]), m1[e]), y[1][2 * (i + e)], y[1][2 * (i + e) + 1]);
+            }
           }
           // a thread writes its own row, 64 dims in a piece: whole sectors, and no staging that the next item's
           // queries would have to wait for
@@ -901,18 +921,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
-              for (int i = 0; i < 8; ++i) dst[(8 * c + i) * 256] = make_float4(v[c][4 * i], v[c][4 * i + 1], v[c][4 * i + 2], v[c][4 * i + 3]);
+              for (int i = 0; i < 8; ++i) dst[(8 * c + i) * 256] = make_float4(y[c][4 * i], y[c][4 * i + 1], y[c][4 * i + 2], y[c][4 * i + 3]);
           } else if (in_item < n_rows) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               if constexpr (kExact) {
                 float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + off + 64 * sp + 32 * c);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[c][4 * i], v[c][4 * i + 1], v[c][4 * i + 2], v[c][4 * i + 3]);
+                for (int i = 0; i < 8; ++i) dst[i] = make_float4(y[c][4 * i], y[c][4 * i + 1], y[c][4 * i + 2], y[c][4 * i + 3]);
               } else {
                 uint16_t* dst = static_cast<uint16_t*>(p.out) + off + 64 * sp + 32 * c;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) store8_bf16(dst + 8 * i, &v[c][8 * i]);
+                for (int i = 0; i < 4; ++i) store8_bf16(dst + 8 * i, &y[c][8 * i]);
               }
             }
           }
@@ -1012,57 +1032,86 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         }
       }
     } else {
-      // =========================================================== rank 0: MMA issuer (one thread)
-      if (lane == 0) {
-        constexpr uint32_t idesc_qk = tc_idesc(2 * kPfRows, kTile, 0);
-        constexpr uint32_t idesc_pv = tc_idesc(2 * kPfRows, kD, 1);
-        const uint64_t q0 = tc_sdesc(sbase, 16, 1024);
-        int t = 0, s = 0;
-        bool ok = true;
-        while (ok && walk.next(g)) {
-          if (!(ok = bounded_wait(bar(kRgQFull), s & 1) && bounded_wait(bar(kRgQPeer), s & 1))) break;
-          ++s;
-          for (int j = 0; j <= g.n; ++j) {
-            if (j < g.n) {   // S[u & 1] = Q K^T
-              const int u = t + j, st = u % kStages;
-              const uint32_t par = (u / kStages) & 1;
-              if (!(ok = bounded_wait(bar(kRgKFull + st), par) && bounded_wait(bar(kRgKPeer + st), par))) break;
-              tc_fence_after();
-              const uint32_t s_t = tmem + 128 * (u & 1);
+      // =========================================================== rank 0: MMA issuer
+      // A wait on a barrier that has long completed costs some 230 cycles here, so the warp's lanes look at all
+      // barriers of a burst at once, and in the middle of the burst before it; lane 0 issues.
+      constexpr uint32_t idesc_qk = tc_idesc(2 * kPfRows, kTile, 0);
+      constexpr uint32_t idesc_pv = tc_idesc(2 * kPfRows, kD, 1);
+      const uint64_t q0 = tc_sdesc(sbase, 16, 1024);
+      // lane i's barrier of a QK (2) or a PV (3; 4 with the last item's rows), and its parity
+      auto kbar = [&](int u) -> uint32_t { return bar((lane == 0 ? kRgKFull : kRgKPeer) + u % kStages); };
+      auto vbar = [&](int u) -> uint32_t {
+        return bar(lane == 0 ? kRgVFull + u % kStages : lane == 1 ? kRgVPeer + u % kStages : lane == 2 ? kRgPFull + (u & 1) : kRgOFree);
+      };
+      auto vpar = [&](int u, int s) -> uint32_t { return lane < 2 ? (u / kStages) & 1 : lane == 2 ? (u >> 1) & 1 : s & 1; };
+      auto look = [&](uint32_t b, uint32_t parity, int n) -> bool {
+        return __all_sync(0xffffffffu, lane >= n || mbar_test_wait(b, parity));
+      };
+      auto wait_all = [&](uint32_t b, uint32_t parity, int n) -> bool { return __all_sync(0xffffffffu, lane >= n || bounded_wait(b, parity)); };
+      int t = 0, s = 0;
+      bool ok = true, k_seen = false;
+      while (ok && walk.next(g)) {
+        ok = wait_all(bar(lane == 0 ? kRgQFull : kRgQPeer), s & 1, 2);
+        if (!ok) break;
+        ++s;
+        for (int j = 0; j <= g.n; ++j) {
+          const int up = t + j - 1, n_pv = j == 1 && s > 1 ? 4 : 3;
+          bool pv_seen = false;
+          if (j < g.n) {   // S[u & 1] = Q K^T
+            const int u = t + j, st = u % kStages;
+            ok = k_seen || wait_all(kbar(u), (u / kStages) & 1, 2);
+            if (!ok) break;
+            k_seen = false;
+            tc_fence_after();
+            const uint32_t s_t = tmem + 128 * (u & 1);
 #pragma unroll
-              for (int x = 0; x < (kExact ? 3 : 1); ++x) {   // Qh Kh, Ql Kh, Qh Kl
-                const uint64_t qx = q0 + (x == 1 ? (Sh::kQPart >> 4) : 0);
-                const uint64_t kx = tc_sdesc(sbase + Sh::kKOff + (st * Sh::kParts + (x == 2 ? 1 : 0)) * Sh::kKPart, 16, 1024);
+            for (int x = 0; x < (kExact ? 3 : 1); ++x) {   // Qh Kh, Ql Kh, Qh Kl
+              const uint64_t qx = q0 + (x == 1 ? (Sh::kQPart >> 4) : 0);
+              const uint64_t kx = tc_sdesc(sbase + Sh::kKOff + (st * Sh::kParts + (x == 2 ? 1 : 0)) * Sh::kKPart, 16, 1024);
 #pragma unroll
-                for (int kk = 0; kk < 16; ++kk)
-                  tc2_mma_ss(s_t, qx + (((kk >> 2) * Sh::kQPanel + (kk & 3) * 32) >> 4), kx + (((kk >> 2) * Sh::kKPanel + (kk & 3) * 32) >> 4),
-                             idesc_qk, (x > 0 || kk > 0) ? 1u : 0u);
+              for (int q = 0; q < 2; ++q) {
+                if (lane == 0) {
+#pragma unroll
+                  for (int kk = 8 * q; kk < 8 * q + 8; ++kk)
+                    tc2_mma_ss(s_t, qx + (((kk >> 2) * Sh::kQPanel + (kk & 3) * 32) >> 4), kx + (((kk >> 2) * Sh::kKPanel + (kk & 3) * 32) >> 4),
+                               idesc_qk, (x > 0 || kk > 0) ? 1u : 0u);
+                }
+                __syncwarp();
+                if (j > 0 && !pv_seen && (q == 0 || kExact)) pv_seen = look(vbar(up), vpar(up, s), n_pv);
               }
+            }
+            if (lane == 0) {
               tc2_commit_both(bar(kRgSFull + (u & 1)));
               if (j == g.n - 1) tc2_commit_both(bar(kRgQFree));
             }
-            if (j > 0) {   // O += P V of tile j - 1
-              const int u = t + j - 1, st = u % kStages;
-              const uint32_t par = (u / kStages) & 1;
-              if (!(ok = bounded_wait(bar(kRgVFull + st), par) && bounded_wait(bar(kRgVPeer + st), par) &&
-                         bounded_wait(bar(kRgPFull + (u & 1)), (u >> 1) & 1) &&
-                         (j > 1 || s < 2 || bounded_wait(bar(kRgOFree), s & 1))))   // the last item's rows have been read
-                break;
-              tc_fence_after();
-              const uint32_t p_t = tmem + 128 * (u & 1);
-#pragma unroll
-              for (int x = 0; x < (kExact ? 3 : 1); ++x) {   // Ph Vh, Pl Vh, Ph Vl
-                const uint64_t vx = tc_sdesc(sbase + Sh::kVOff + (st * Sh::kParts + (x == 2 ? 1 : 0)) * Sh::kVPart, Sh::kVPanel, 1024);
-#pragma unroll
-                for (int ks = 0; ks < kTile / 16; ++ks)
-                  tc2_mma_ts(tmem + kTmO, p_t + (x == 1 ? 32 : 0) + 8 * ks, vx + ((ks * 16 * 128) >> 4), idesc_pv,
-                             (j > 1 || x > 0 || ks > 0) ? 1u : 0u);
-              }
-              tc2_commit_both(bar(kRgVEmpty + (u & 1)));
-            }
           }
-          t += g.n;
+          if (j > 0) {   // O += P V of tile j - 1
+            const int st = up % kStages;
+            ok = pv_seen || wait_all(vbar(up), vpar(up, s), n_pv);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t p_t = tmem + 128 * (up & 1);
+#pragma unroll
+            for (int x = 0; x < (kExact ? 3 : 1); ++x) {   // Ph Vh, Pl Vh, Ph Vl
+              const uint64_t vx = tc_sdesc(sbase + Sh::kVOff + (st * Sh::kParts + (x == 2 ? 1 : 0)) * Sh::kVPart, Sh::kVPanel, 1024);
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                if (lane == 0) {
+#pragma unroll
+                  for (int ks = q * (kTile / 32); ks < (q + 1) * (kTile / 32); ++ks)
+                    tc2_mma_ts(tmem + kTmO, p_t + (x == 1 ? 32 : 0) + 8 * ks, vx + ((ks * 16 * 128) >> 4), idesc_pv,
+                               (j > 1 || x > 0 || ks > 0) ? 1u : 0u);
+                }
+                __syncwarp();
+                if (j + 1 < g.n && !k_seen && q == 0) k_seen = look(kbar(t + j + 1), ((t + j + 1) / kStages) & 1, 2);
+              }
+            }
+            if (lane == 0) tc2_commit_both(bar(kRgVEmpty + (up & 1)));
+          }
         }
+        t += g.n;
+      }
+      if (lane == 0) {
         // every MMA that this thread issued has completed before TMEM is released
         tc2_commit_own(bar(kRgDrain));
         drain(bar(kRgDrain), 0);
