@@ -32,7 +32,8 @@
 //   warp 8     K tiles (its half of each tile's positions) and the values' sizes
 //   warp 9     rank 0: issues every tcgen05.mma of the pair, QK(j) then PV(j - 1);
 //              rank 1: tells rank 0 when its own copies have landed
-//   warp 10    V tiles (its half of the dims)      warp 11  Q rows
+//   warp 10    V tiles (its half of the dims)
+//   warp 11    Q rows, and what the softmax has to know of the item, ahead of it
 // A vector with an infinity or a NaN (or too large for the rows) becomes a key row of NaN and a
 // value row of zeros: a mask takes its score away whole, so only those who see it feel it.
 // bf16 results: single f16 operands (queries, centroids, weights: each rounded once, 2^-11
@@ -68,7 +69,9 @@ struct RgShape {
   static constexpr uint32_t kMaxOff = kNormOff + kRgNormSlots * kTile * 4;   // [2][2 halves][128] f32: row maxima
   static constexpr uint32_t kSumOff = kMaxOff + 2 * 2 * kPfRows * 4;         // [2 halves][128] f32: row sums
   static constexpr uint32_t kSignOff = kSumOff + 2 * kPfRows * 4;            // [256] f32: the rotation's signs
-  static constexpr uint32_t kBarOff = kSignOff + kD * 4;
+  static constexpr uint32_t kItemOff = kSignOff + kD * 4;                    // [4] RgItem
+  static constexpr uint32_t kFacOff = kItemOff + 4 * 64;                     // [4][128] f32: the rows' score factors
+  static constexpr uint32_t kBarOff = kFacOff + 4 * kPfRows * 4;
   static constexpr uint32_t kMiscOff = kBarOff + 256;         // [0] TMEM base, [1] abort
   static constexpr uint32_t kSmem = kMiscOff + 64 + 1024;     // + alignment slack
   static constexpr float kLazy = kExact ? 0.f : 4.f;           // P = p n_v / 16 <= 2^4 * 65504 / 16; fp32: p <= 1, P = p n_v
@@ -520,14 +523,24 @@ __global__ void __launch_bounds__(kRgPrepThreads) ragged_prep_kernel(const Ragge
   }
 }
 
-// 16 and 64 consecutive TMEM columns of this thread's lane (load and wait in one statement, as tm_ld32)
-__device__ __forceinline__ void tm_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+// Four times 16 TMEM columns of this thread's lane, 64 apart, and 64 consecutive ones (loads and wait in one
+// statement, as tm_ld32)
+__device__ __forceinline__ void tm_ld16x4(uint32_t taddr, uint32_t (&r)[4][16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%64];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%65];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47}, [%66];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%67];\n"
       "tcgen05.wait::ld.sync.aligned;\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
+      : "=r"(r[0][0]), "=r"(r[0][1]), "=r"(r[0][2]), "=r"(r[0][3]), "=r"(r[0][4]), "=r"(r[0][5]), "=r"(r[0][6]), "=r"(r[0][7]),
+        "=r"(r[0][8]), "=r"(r[0][9]), "=r"(r[0][10]), "=r"(r[0][11]), "=r"(r[0][12]), "=r"(r[0][13]), "=r"(r[0][14]), "=r"(r[0][15]),
+        "=r"(r[1][0]), "=r"(r[1][1]), "=r"(r[1][2]), "=r"(r[1][3]), "=r"(r[1][4]), "=r"(r[1][5]), "=r"(r[1][6]), "=r"(r[1][7]),
+        "=r"(r[1][8]), "=r"(r[1][9]), "=r"(r[1][10]), "=r"(r[1][11]), "=r"(r[1][12]), "=r"(r[1][13]), "=r"(r[1][14]), "=r"(r[1][15]),
+        "=r"(r[2][0]), "=r"(r[2][1]), "=r"(r[2][2]), "=r"(r[2][3]), "=r"(r[2][4]), "=r"(r[2][5]), "=r"(r[2][6]), "=r"(r[2][7]),
+        "=r"(r[2][8]), "=r"(r[2][9]), "=r"(r[2][10]), "=r"(r[2][11]), "=r"(r[2][12]), "=r"(r[2][13]), "=r"(r[2][14]), "=r"(r[2][15]),
+        "=r"(r[3][0]), "=r"(r[3][1]), "=r"(r[3][2]), "=r"(r[3][3]), "=r"(r[3][4]), "=r"(r[3][5]), "=r"(r[3][6]), "=r"(r[3][7]),
+        "=r"(r[3][8]), "=r"(r[3][9]), "=r"(r[3][10]), "=r"(r[3][11]), "=r"(r[3][12]), "=r"(r[3][13]), "=r"(r[3][14]), "=r"(r[3][15])
+      : "r"(taddr), "r"(taddr + 64), "r"(taddr + 128), "r"(taddr + 192)
       : "memory");
 }
 __device__ __forceinline__ void tm_ld64(uint32_t taddr, uint32_t (&r)[64]) {
@@ -556,6 +569,13 @@ struct RgSeg {
   int32_t head, blk, tile, n, all;
   int32_t part;   // partial rows' index, -1: the whole item
 };
+// What the softmax needs of a stretch, laid out by the warp that loads its queries
+struct RgItem {
+  int32_t n, tile, sinks, skip;     // tiles, the first one; tiles of sinks, gap after them
+  int32_t first, row, n_rows, head; // position of the request's first new token; first row within the request; rows
+  int32_t row0, part, pad[2];
+};
+static_assert(sizeof(RgItem) <= 64, "item records");
 // The pair's stretches in order; every warp walks them by itself.
 struct RgWalk {
   const RaggedParams& p;
@@ -593,14 +613,14 @@ struct RgWalk {
   }
 };
 
-// one look at a barrier's phase
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+// one look at a barrier's phase (1: complete)
+__device__ __forceinline__ uint32_t mbar_look(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
                : "=r"(done)
                : "r"(bar), "r"(parity)
                : "memory");
-  return done != 0;
+  return done;
 }
 // One arrival on a barrier of the pair, at its default scope. What it orders lies in tensor memory
 // (ordered by the tcgen05 fences on both sides) or was written by a copy that has completed: no
@@ -741,6 +761,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
   if (pair < p.head->n_pairs) {
     RgWalk walk(p, pair);
     RgSeg g;
+    // registers: 384 x 168 at launch = 256 x 200 + 128 x 104
+    if (w < kRgSoftWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;\n");
     if (w < kRgSoftWarps) {
       // =========================================================== softmax / epilogue
       constexpr int kC = kTile / 2;                 // columns of this thread
@@ -749,6 +772,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
       const uint32_t lane_addr = tmem + (uint32_t(32 * quad) << 16);
       const float* norms = reinterpret_cast<const float*>(smem + Sh::kNormOff) + kC * half;
       int t = 0;      // tiles of this pair so far
+      int64_t left = walk.left;
       bool ok = true;
       // The two warps of these rows swap a value per row through buf and agree on going on, so that after a wait
       // that gave up both leave at the same meeting (the value is then kRgGone).
@@ -759,21 +783,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         ok = ok && __float_as_uint(other) != kRgGone;
         return other;
       };
-      while (ok && walk.next(g)) {
-        const RgReq rq = p.req[p.blk_req[g.blk]];
-        const int rb = g.blk - rq.blk0;
-        const RgSpan span = rg_block_span<kTile>(p, rq, rb);
-        const int n_rows = min(256, 6 * rq.n_new - 256 * rb);       // the item's rows
-        const int row = min(int(rank) * kPfRows + r_local, n_rows - 1);   // padding rows repeat the last
-        const int P = rq.first + (256 * rb + row) / 6;              // this row's position
-        const float fac = p.qfac[int64_t(g.head) * kGroup * p.n_tok + int64_t(rq.row0) * kGroup + 256 * rb + row];
+      int item = 0;
+      while (ok && left > 0) {
+        // the item's first scores have been made from its queries, so its record is there
+        ok = warp_wait(bar(kRgNFull + (t & 3)), (t >> 2) & 1) && warp_wait(bar(kRgSFull + (t & 1)), (t >> 1) & 1);
+        const RgItem it = *reinterpret_cast<const RgItem*>(smem + Sh::kItemOff + (item & 3) * 64);
+        const float fac = reinterpret_cast<const float*>(smem + Sh::kFacOff)[(item & 3) * kPfRows + r_local];
+        ++item;
+        const int n = ok ? it.n : 1;   // (no record after a wait that gave up: one round to the meeting where both leave)
+        left -= n;
+        const int row = min(int(rank) * kPfRows + r_local, it.n_rows - 1);   // padding rows repeat the last
+        const int P = it.first + (it.row + row) / 6;                          // this row's position
         float m_ref = -INFINITY, l_sum = 0.f;
         bool left_early = false;
-        for (int j = 0; j < g.n; ++j, ++t) {
+        for (int j = 0; j < n; ++j, ++t) {
           const int b = t & 1;
-          const int at = g.tile + j;
-          const int pos0 = (at < span.sinks ? at : at + span.skip) * kTile + kC * half;   // of this thread's columns
-          ok = ok && warp_wait(bar(kRgNFull + (t & 3)), (t >> 2) & 1) && warp_wait(bar(kRgSFull + b), (t >> 1) & 1);
+          const int at = it.tile + j;
+          const int pos0 = (at < it.sinks ? at : at + it.skip) * kTile + kC * half;   // of this thread's columns
+          if (j > 0) ok = ok && warp_wait(bar(kRgNFull + (t & 3)), (t >> 2) & 1) && warp_wait(bar(kRgSFull + b), (t >> 1) & 1);
           tc_fence_after();
           uint32_t sr[kC];
           float mx = -INFINITY;
@@ -868,12 +895,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         const float rest = swap(reinterpret_cast<float*>(smem + Sh::kSumOff), l_sum);
         if (!ok) break;
         l_sum += rest;
-        const bool whole = g.part < 0;
+        const bool whole = it.part < 0;
         const float inv = !whole ? 0.0625f / Sh::kPScale : l_sum == 0.f ? 0.f : (0.0625f / Sh::kPScale) / l_sum;
         const int in_item = int(rank) * kPfRows + r_local;     // this thread's row of the item
-        if (!whole && half == 0) p.pml[int64_t(g.part) * 256 + in_item] = make_float2(m_ref, l_sum);
-        const int ir = 256 * rb + in_item, tok = rq.row0 + ir / 6, jh = ir % 6;
-        const int64_t off = (int64_t(tok) * kHq + g.head * kGroup + jh) * kD + 128 * half;
+        if (!whole && half == 0) p.pml[int64_t(it.part) * 256 + in_item] = make_float2(m_ref, l_sum);
+        const int ir = it.row + in_item, tok = it.row0 + ir / 6, jh = ir % 6;
+        const int64_t off = (int64_t(tok) * kHq + it.head * kGroup + jh) * kD + 128 * half;
         const float i7 = half ? -inv : inv;
         const float4* const sgn4 = reinterpret_cast<const float4*>(smem + Sh::kSignOff) + 32 * half;
 #pragma unroll 1
@@ -884,16 +911,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {   // 16 dims at a time
             uint64_t* const x = v[c >> 1] + 8 * (c & 1);
+            uint32_t o[4][16];
+            tm_ld16x4(lane_addr + kTmO + 16 * c, o);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t o[16];
-              tm_ld16(lane_addr + kTmO + 64 * k + 16 * c, o);
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const uint64_t y = pair_f32(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+                const uint64_t y = pair_f32(__uint_as_float(o[k][2 * i]), __uint_as_float(o[k][2 * i + 1]));
                 x[i] = k == 0 ? mul2_f32(y, f[0]) : fma2_f32(y, f[k], x[i]);
               }
-            }
           }
           if (sp == 1) {   // O has been read: the next item's first PV may replace it
             tc_fence_before();
@@ -917,12 +943,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
           // a thread writes its own row, 64 dims in a piece: whole sectors, and no staging that the next item's
           // queries would have to wait for
           if (!whole) {   // [part][dims / 4][row]: the lanes' pieces lie side by side
-            float4* dst = reinterpret_cast<float4*>(p.po) + (int64_t(g.part) * 64 + 32 * half + 16 * sp) * 256 + in_item;
+            float4* dst = reinterpret_cast<float4*>(p.po) + (int64_t(it.part) * 64 + 32 * half + 16 * sp) * 256 + in_item;
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int i = 0; i < 8; ++i) dst[(8 * c + i) * 256] = make_float4(y[c][4 * i], y[c][4 * i + 1], y[c][4 * i + 2], y[c][4 * i + 3]);
-          } else if (in_item < n_rows) {
+          } else if (in_item < it.n_rows) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               if constexpr (kExact) {
@@ -990,23 +1016,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         }
       }
     } else if (w == kRgQWarp) {
-      // =========================================================== Q rows, one item at a time
-      if (lane == 0) {
-        int s = 0;
-        while (walk.next(g)) {
-          const RgReq rq = p.req[p.blk_req[g.blk]];
-          const int64_t row = int64_t(g.head) * kGroup * p.n_tok + int64_t(rq.row0) * kGroup + 256 * (g.blk - rq.blk0) + int(rank) * kPfRows;
-          if (s > 0 && !bounded_wait(bar(kRgQFree), (s - 1) & 1)) break;   // the last item's last QK has run
+      // =========================================================== Q rows and the item's record
+      int s = 0;
+      while (walk.next(g)) {
+        const RgReq rq = p.req[p.blk_req[g.blk]];
+        const int rb = g.blk - rq.blk0, n_rows = min(256, 6 * rq.n_new - 256 * rb);
+        const int64_t row = int64_t(g.head) * kGroup * p.n_tok + int64_t(rq.row0) * kGroup + 256 * rb;
+        // Slot s & 3 held item s - 4. Here item s - 2's last QK has run; it was issued after item s - 3's PV, which
+        // takes that item's P: the softmax has read the records up to s - 3.
+        float* const fac = reinterpret_cast<float*>(smem + Sh::kFacOff) + (s & 3) * kPfRows;
+#pragma unroll
+        for (int i = 0; i < kPfRows / 32; ++i) fac[32 * i + lane] = p.qfac[row + min(int(rank) * kPfRows + 32 * i + lane, n_rows - 1)];
+        if (lane == 0) {
+          const RgSpan span = rg_block_span<kTile>(p, rq, rb);
+          *reinterpret_cast<RgItem*>(smem + Sh::kItemOff + (s & 3) * 64) =
+              RgItem{g.n, g.tile, span.sinks, span.skip, rq.first, 256 * rb, n_rows, g.head, rq.row0, g.part, {0, 0}};
+        }
+        __syncwarp();
+        bool ok = true;
+        if (lane == 0 && s > 0) ok = bounded_wait(bar(kRgQFree), (s - 1) & 1);   // the last item's last QK has run
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (lane == 0) {
           mbar_expect_tx(bar(kRgQFull), Sh::kParts * Sh::kQPart);
 #pragma unroll
           for (int x = 0; x < Sh::kParts; ++x)
 #pragma unroll
             for (int d = 0; d < 4; ++d)
-              tma_load_2d(sbase + x * Sh::kQPart + d * Sh::kQPanel, &qmap, 64 * d, int(x * int64_t(kHq) * p.n_tok + row), bar(kRgQFull));
-          ++s;
+              tma_load_2d(sbase + x * Sh::kQPart + d * Sh::kQPanel, &qmap, 64 * d, int(x * int64_t(kHq) * p.n_tok + row + int(rank) * kPfRows),
+                          bar(kRgQFull));
         }
-        if (misc[1] && s > 0) drain(bar(kRgQFull), (s - 1) & 1);
+        ++s;
       }
+      if (lane == 0 && misc[1] && s > 0) drain(bar(kRgQFull), (s - 1) & 1);
     } else if (rank == 1) {
       // =========================================================== rank 1: its copies have landed
       if (lane == 0) {
@@ -1032,86 +1073,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         }
       }
     } else {
-      // =========================================================== rank 0: MMA issuer
-      // A wait on a barrier that has long completed costs some 230 cycles here, so the warp's lanes look at all
-      // barriers of a burst at once, and in the middle of the burst before it; lane 0 issues.
-      constexpr uint32_t idesc_qk = tc_idesc(2 * kPfRows, kTile, 0);
-      constexpr uint32_t idesc_pv = tc_idesc(2 * kPfRows, kD, 1);
-      const uint64_t q0 = tc_sdesc(sbase, 16, 1024);
-      // lane i's barrier of a QK (2) or a PV (3; 4 with the last item's rows), and its parity
-      auto kbar = [&](int u) -> uint32_t { return bar((lane == 0 ? kRgKFull : kRgKPeer) + u % kStages); };
-      auto vbar = [&](int u) -> uint32_t {
-        return bar(lane == 0 ? kRgVFull + u % kStages : lane == 1 ? kRgVPeer + u % kStages : lane == 2 ? kRgPFull + (u & 1) : kRgOFree);
-      };
-      auto vpar = [&](int u, int s) -> uint32_t { return lane < 2 ? (u / kStages) & 1 : lane == 2 ? (u >> 1) & 1 : s & 1; };
-      auto look = [&](uint32_t b, uint32_t parity, int n) -> bool {
-        return __all_sync(0xffffffffu, lane >= n || mbar_test_wait(b, parity));
-      };
-      auto wait_all = [&](uint32_t b, uint32_t parity, int n) -> bool { return __all_sync(0xffffffffu, lane >= n || bounded_wait(b, parity)); };
-      int t = 0, s = 0;
-      bool ok = true, k_seen = false;
-      while (ok && walk.next(g)) {
-        ok = wait_all(bar(lane == 0 ? kRgQFull : kRgQPeer), s & 1, 2);
-        if (!ok) break;
-        ++s;
-        for (int j = 0; j <= g.n; ++j) {
-          const int up = t + j - 1, n_pv = j == 1 && s > 1 ? 4 : 3;
-          bool pv_seen = false;
-          if (j < g.n) {   // S[u & 1] = Q K^T
-            const int u = t + j, st = u % kStages;
-            ok = k_seen || wait_all(kbar(u), (u / kStages) & 1, 2);
-            if (!ok) break;
-            k_seen = false;
-            tc_fence_after();
-            const uint32_t s_t = tmem + 128 * (u & 1);
+      // =========================================================== rank 0: MMA issuer (one thread)
+      // A look at a barrier queues behind the products issued before it and takes 250 cycles and more, and the
+      // tensor pipe runs dry meanwhile. So the next burst's barriers are looked at in the middle of this one, the
+      // answers are taken at its end, and only a barrier not yet seen complete is waited for.
+      if (lane == 0) {
+        constexpr uint32_t idesc_qk = tc_idesc(2 * kPfRows, kTile, 0);
+        constexpr uint32_t idesc_pv = tc_idesc(2 * kPfRows, kD, 1);
+        const uint64_t q0 = tc_sdesc(sbase, 16, 1024);
+        int t = 0, s = 0;
+        bool ok = true;
+        while (ok && walk.next(g)) {
+          if (!(ok = bounded_wait(bar(kRgQFull), s & 1) && bounded_wait(bar(kRgQPeer), s & 1))) break;
+          ++s;
+          uint32_t k_seen = 0;
+          for (int j = 0; j <= g.n; ++j) {
+            const int up = t + j - 1, vst = up & (kStages - 1);   // tile of this round's PV
+            const uint32_t vpar = (up / kStages) & 1, ppar = (up >> 1) & 1;
+            uint32_t pv_seen = 0;
+            if (j < g.n) {   // S[u & 1] = Q K^T
+              const int u = t + j, st = u & (kStages - 1);
+              const uint32_t par = (u / kStages) & 1;
+              if (!k_seen && !(ok = bounded_wait(bar(kRgKFull + st), par) && bounded_wait(bar(kRgKPeer + st), par))) break;
+              tc_fence_after();
+              const uint32_t s_t = tmem + 128 * (u & 1);
 #pragma unroll
-            for (int x = 0; x < (kExact ? 3 : 1); ++x) {   // Qh Kh, Ql Kh, Qh Kl
-              const uint64_t qx = q0 + (x == 1 ? (Sh::kQPart >> 4) : 0);
-              const uint64_t kx = tc_sdesc(sbase + Sh::kKOff + (st * Sh::kParts + (x == 2 ? 1 : 0)) * Sh::kKPart, 16, 1024);
+              for (int x = 0; x < (kExact ? 3 : 1); ++x) {   // Qh Kh, Ql Kh, Qh Kl
+                const uint64_t qx = q0 + (x == 1 ? (Sh::kQPart >> 4) : 0);
+                const uint64_t kx = tc_sdesc(sbase + Sh::kKOff + (st * Sh::kParts + (x == 2 ? 1 : 0)) * Sh::kKPart, 16, 1024);
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                if (lane == 0) {
-#pragma unroll
-                  for (int kk = 8 * q; kk < 8 * q + 8; ++kk)
-                    tc2_mma_ss(s_t, qx + (((kk >> 2) * Sh::kQPanel + (kk & 3) * 32) >> 4), kx + (((kk >> 2) * Sh::kKPanel + (kk & 3) * 32) >> 4),
-                               idesc_qk, (x > 0 || kk > 0) ? 1u : 0u);
+                for (int kk = 0; kk < 16; ++kk) {
+                  tc2_mma_ss(s_t, qx + (((kk >> 2) * Sh::kQPanel + (kk & 3) * 32) >> 4), kx + (((kk >> 2) * Sh::kKPanel + (kk & 3) * 32) >> 4),
+                             idesc_qk, (x > 0 || kk > 0) ? 1u : 0u);
+                  if (x == (kExact ? 2 : 0) && kk == 11)
+                    pv_seen = mbar_look(bar(kRgVFull + vst), vpar) & mbar_look(bar(kRgVPeer + vst), vpar) & mbar_look(bar(kRgPFull + (up & 1)), ppar) &
+                              (j > 0 ? 1u : 0u);
                 }
-                __syncwarp();
-                if (j > 0 && !pv_seen && (q == 0 || kExact)) pv_seen = look(vbar(up), vpar(up, s), n_pv);
               }
-            }
-            if (lane == 0) {
               tc2_commit_both(bar(kRgSFull + (u & 1)));
               if (j == g.n - 1) tc2_commit_both(bar(kRgQFree));
             }
-          }
-          if (j > 0) {   // O += P V of tile j - 1
-            const int st = up % kStages;
-            ok = pv_seen || wait_all(vbar(up), vpar(up, s), n_pv);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t p_t = tmem + 128 * (up & 1);
+            k_seen = 0;
+            if (j > 0) {   // O += P V of tile j - 1
+              if (!pv_seen && !(ok = bounded_wait(bar(kRgVFull + vst), vpar) && bounded_wait(bar(kRgVPeer + vst), vpar) &&
+                                     bounded_wait(bar(kRgPFull + (up & 1)), ppar)))
+                break;
+              if (j == 1 && s > 1 && !(ok = bounded_wait(bar(kRgOFree), s & 1))) break;   // the last item's rows have been read
+              tc_fence_after();
+              const uint32_t p_t = tmem + 128 * (up & 1);
+              const int un = t + j + 1, nst = un & (kStages - 1);   // the next round's QK
+              const uint32_t npar = (un / kStages) & 1;
 #pragma unroll
-            for (int x = 0; x < (kExact ? 3 : 1); ++x) {   // Ph Vh, Pl Vh, Ph Vl
-              const uint64_t vx = tc_sdesc(sbase + Sh::kVOff + (st * Sh::kParts + (x == 2 ? 1 : 0)) * Sh::kVPart, Sh::kVPanel, 1024);
+              for (int x = 0; x < (kExact ? 3 : 1); ++x) {   // Ph Vh, Pl Vh, Ph Vl
+                const uint64_t vx = tc_sdesc(sbase + Sh::kVOff + (vst * Sh::kParts + (x == 2 ? 1 : 0)) * Sh::kVPart, Sh::kVPanel, 1024);
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                if (lane == 0) {
-#pragma unroll
-                  for (int ks = q * (kTile / 32); ks < (q + 1) * (kTile / 32); ++ks)
-                    tc2_mma_ts(tmem + kTmO, p_t + (x == 1 ? 32 : 0) + 8 * ks, vx + ((ks * 16 * 128) >> 4), idesc_pv,
-                               (j > 1 || x > 0 || ks > 0) ? 1u : 0u);
+                for (int ks = 0; ks < kTile / 16; ++ks) {
+                  tc2_mma_ts(tmem + kTmO, p_t + (x == 1 ? 32 : 0) + 8 * ks, vx + ((ks * 16 * 128) >> 4), idesc_pv, (j > 1 || x > 0 || ks > 0) ? 1u : 0u);
+                  if (x == (kExact ? 2 : 0) && ks == kTile / 32)
+                    k_seen = mbar_look(bar(kRgKFull + nst), npar) & mbar_look(bar(kRgKPeer + nst), npar) & (j + 1 < g.n ? 1u : 0u);
                 }
-                __syncwarp();
-                if (j + 1 < g.n && !k_seen && q == 0) k_seen = look(kbar(t + j + 1), ((t + j + 1) / kStages) & 1, 2);
               }
+              tc2_commit_both(bar(kRgVEmpty + (up & 1)));
             }
-            if (lane == 0) tc2_commit_both(bar(kRgVEmpty + (up & 1)));
           }
+          t += g.n;
         }
-        t += g.n;
-      }
-      if (lane == 0) {
         // every MMA that this thread issued has completed before TMEM is released
         tc2_commit_own(bar(kRgDrain));
         drain(bar(kRgDrain), 0);
