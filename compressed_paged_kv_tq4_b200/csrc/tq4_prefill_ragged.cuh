@@ -28,12 +28,19 @@
 //   warps 0-7  softmax: warps w and w + 4 share 32 rows, half of the columns each, one thread
 //              per row: scores from TMEM, mask, running maximum (exchanged through shared
 //              memory; raised only when it grows by more than 2^4), P = p * n_v written over
-//              the scores as f16; the epilogue: O / l, R^T by in-register butterflies, out.
+//              the scores as f16, the first 64 positions' ahead of the others'; the epilogue:
+//              O / l, R^T by in-register butterflies, out.
 //   warp 8     K tiles (its half of each tile's positions) and the values' sizes
-//   warp 9     rank 0: issues every tcgen05.mma of the pair, QK(j) then PV(j - 1);
-//              rank 1: tells rank 0 when its own copies have landed
-//   warp 10    V tiles (its half of the dims)
-//   warp 11    Q rows, and what the softmax has to know of the item, ahead of it
+//   warp 9     rank 0: one thread issues every tcgen05.mma of the pair, QK(j + 1), then PV(j);
+//              rank 1: tells rank 0 when its Q rows and K tiles have landed
+//   warp 10    Q rows, what the softmax has to know of the item, and V tiles (its half of the dims)
+//   warp 11    rank 0: gathers both CTAs' copies into one barrier before each product;
+//              rank 1: tells rank 0 of its V tiles
+// A tile costs 2,048 cycles of the tensor pipe. What has to be short for that is the loop scores ->
+// softmax -> PV -> the next QK into the same buffer (two of them): at 5,400 cycles it held a tile at
+// 2,700 to 3,000. So the issuer waits once before each of its three bursts (a wait takes 250 cycles;
+// five of them did not fit), PV starts on the first half of P, and products order one another by the
+// issue order of one thread, not by barriers.
 // A vector with an infinity or a NaN (or too large for the rows) becomes a key row of NaN and a
 // value row of zeros: a mask takes its score away whole, so only those who see it feel it.
 // bf16 results: single f16 operands (queries, centroids, weights: each rounded once, 2^-11
@@ -48,7 +55,7 @@
 
 namespace tq4 {
 
-constexpr int kRgSoftWarps = 8, kRgKWarp = 8, kRgMmaWarp = 9, kRgVWarp = 10, kRgQWarp = 11;
+constexpr int kRgSoftWarps = 8, kRgKWarp = 8, kRgMmaWarp = 9, kRgVWarp = 10;   // 11: gathers
 constexpr int kRgThreads = 32 * 12;
 constexpr int kRgNormSlots = 4;
 constexpr int kRgMinTiles = 256;      // positions: a pair's share is at least this many (a few tiles)
@@ -81,7 +88,7 @@ static_assert(RgShape<false>::kSmem <= 227u * 1024u && RgShape<true>::kSmem <= 2
 
 // barriers (8 B each)
 constexpr int kRgQFull = 0, kRgQPeer = 1, kRgKFull = 2, kRgKPeer = 4, kRgVFull = 6, kRgVPeer = 8, kRgNFull = 10,
-              kRgPFull = 14, kRgSFull = 16, kRgVEmpty = 18, kRgOFree = 20, kRgDrain = 21, kRgQFree = 22;
+              kRgKReady = 14, kRgPFull = 16, kRgPRest = 18, kRgSFull = 20, kRgVEmpty = 22, kRgQFree = 24, kRgDrain = 25;
 
 struct RgReq {
   int32_t row0, n_new;   // rows of q, k, v; 0 new tokens for a request without work
@@ -523,7 +530,7 @@ __global__ void __launch_bounds__(kRgPrepThreads) ragged_prep_kernel(const Ragge
   }
 }
 
-// Four times 16 TMEM columns of this thread's lane, 64 apart, and 64 consecutive ones (loads and wait in one
+// Four times 16 TMEM columns of this thread's lane, 64 apart, and twice 32 columns (loads and wait in one
 // statement, as tm_ld32)
 __device__ __forceinline__ void tm_ld16x4(uint32_t taddr, uint32_t (&r)[4][16]) {
   asm volatile(
@@ -543,24 +550,22 @@ __device__ __forceinline__ void tm_ld16x4(uint32_t taddr, uint32_t (&r)[4][16]) 
       : "r"(taddr), "r"(taddr + 64), "r"(taddr + 128), "r"(taddr + 192)
       : "memory");
 }
-__device__ __forceinline__ void tm_ld64(uint32_t taddr, uint32_t (&r)[64]) {
+__device__ __forceinline__ void tm_ld32x2(uint32_t a0, uint32_t a1, uint32_t (&r)[2][32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
-      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
-      "}, [%64];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n"
       "tcgen05.wait::ld.sync.aligned;\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-      : "r"(taddr)
+      : "=r"(r[0][0]), "=r"(r[0][1]), "=r"(r[0][2]), "=r"(r[0][3]), "=r"(r[0][4]), "=r"(r[0][5]), "=r"(r[0][6]), "=r"(r[0][7]),
+        "=r"(r[0][8]), "=r"(r[0][9]), "=r"(r[0][10]), "=r"(r[0][11]), "=r"(r[0][12]), "=r"(r[0][13]), "=r"(r[0][14]), "=r"(r[0][15]),
+        "=r"(r[0][16]), "=r"(r[0][17]), "=r"(r[0][18]), "=r"(r[0][19]), "=r"(r[0][20]), "=r"(r[0][21]), "=r"(r[0][22]), "=r"(r[0][23]),
+        "=r"(r[0][24]), "=r"(r[0][25]), "=r"(r[0][26]), "=r"(r[0][27]), "=r"(r[0][28]), "=r"(r[0][29]), "=r"(r[0][30]), "=r"(r[0][31]),
+        "=r"(r[1][0]), "=r"(r[1][1]), "=r"(r[1][2]), "=r"(r[1][3]), "=r"(r[1][4]), "=r"(r[1][5]), "=r"(r[1][6]), "=r"(r[1][7]),
+        "=r"(r[1][8]), "=r"(r[1][9]), "=r"(r[1][10]), "=r"(r[1][11]), "=r"(r[1][12]), "=r"(r[1][13]), "=r"(r[1][14]), "=r"(r[1][15]),
+        "=r"(r[1][16]), "=r"(r[1][17]), "=r"(r[1][18]), "=r"(r[1][19]), "=r"(r[1][20]), "=r"(r[1][21]), "=r"(r[1][22]), "=r"(r[1][23]),
+        "=r"(r[1][24]), "=r"(r[1][25]), "=r"(r[1][26]), "=r"(r[1][27]), "=r"(r[1][28]), "=r"(r[1][29]), "=r"(r[1][30]), "=r"(r[1][31])
+      : "r"(a0), "r"(a1)
       : "memory");
 }
 
@@ -613,15 +618,6 @@ struct RgWalk {
   }
 };
 
-// one look at a barrier's phase (1: complete)
-__device__ __forceinline__ uint32_t mbar_look(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-               : "=r"(done)
-               : "r"(bar), "r"(parity)
-               : "memory");
-  return done;
-}
 // One arrival on a barrier of the pair, at its default scope. What it orders lies in tensor memory
 // (ordered by the tcgen05 fences on both sides) or was written by a copy that has completed: no
 // generic-proxy store of this thread has to be seen by the other CTA. A release at cluster scope
@@ -677,11 +673,6 @@ __device__ __forceinline__ float max3_f32(float a, float b, float c) {
   return d;
 }
 constexpr uint32_t kRgGone = 0x7FC0DEADu;   // a NaN that no arithmetic gives
-template <int N>
-__device__ __forceinline__ void rg_ld_scores(uint32_t taddr, uint32_t (&r)[N]) {
-  if constexpr (N == 64) tm_ld64(taddr, r);
-  else tm_ld32(taddr, r);
-}
 
 template <bool kExact>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
@@ -707,12 +698,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
       mbar_init(bar(kRgKPeer + b), 1);
       mbar_init(bar(kRgVFull + b), 1);
       mbar_init(bar(kRgVPeer + b), 1);
-      mbar_init(bar(kRgPFull + b), 2 * kRgSoftWarps);
+      mbar_init(bar(kRgKReady + b), 1);
+      mbar_init(bar(kRgPFull + b), 2 * kRgSoftWarps + 1);   // and the V tile
+      mbar_init(bar(kRgPRest + b), 2 * kRgSoftWarps);
       mbar_init(bar(kRgSFull + b), 1);
       mbar_init(bar(kRgVEmpty + b), 1);
     }
     for (int b = 0; b < kRgNormSlots; ++b) mbar_init(bar(kRgNFull + b), 1);
-    mbar_init(bar(kRgOFree), 2 * kRgSoftWarps);
     mbar_init(bar(kRgDrain), 1);
     mbar_init(bar(kRgQFree), 1);
     misc[1] = 0;
@@ -766,11 +758,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;\n");
     if (w < kRgSoftWarps) {
       // =========================================================== softmax / epilogue
-      constexpr int kC = kTile / 2;                 // columns of this thread
+      constexpr int kHalves = kExact ? 1 : 2;       // P goes out in pieces of 64 positions, 32 columns of each from this thread
       const int quad = w & 3, half = w >> 2;
       const int r_local = 32 * quad + lane;
       const uint32_t lane_addr = tmem + (uint32_t(32 * quad) << 16);
-      const float* norms = reinterpret_cast<const float*>(smem + Sh::kNormOff) + kC * half;
+      const float* norms = reinterpret_cast<const float*>(smem + Sh::kNormOff) + 32 * half;
       int t = 0;      // tiles of this pair so far
       int64_t left = walk.left;
       bool ok = true;
@@ -799,25 +791,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         for (int j = 0; j < n; ++j, ++t) {
           const int b = t & 1;
           const int at = it.tile + j;
-          const int pos0 = (at < it.sinks ? at : at + it.skip) * kTile + kC * half;   // of this thread's columns
+          const int pos0 = (at < it.sinks ? at : at + it.skip) * kTile;
           if (j > 0) ok = ok && warp_wait(bar(kRgNFull + (t & 3)), (t >> 2) & 1) && warp_wait(bar(kRgSFull + b), (t >> 1) & 1);
           tc_fence_after();
-          uint32_t sr[kC];
+          uint32_t sr[kHalves][32];
           float mx = -INFINITY;
           if (ok) {
-            rg_ld_scores<kC>(lane_addr + 128 * b + kC * half, sr);
-            if (!__all_sync(0xffffffffu, pos0 + kC - 1 <= P && (pos0 > P - p.window || pos0 + kC <= p.n_sink))) {
+            const uint32_t s_t = lane_addr + 128 * b + 32 * half;
+            if constexpr (kExact) tm_ld32(s_t, sr[0]);
+            else tm_ld32x2(s_t, s_t + 64, sr);
+            if (!__all_sync(0xffffffffu, pos0 + kTile - 1 <= P && (pos0 > P - p.window || pos0 + kTile <= p.n_sink))) {
 #pragma unroll
-              for (int i = 0; i < kC; ++i) {
-                const int pos = pos0 + i;
-                if (!(pos <= P && (pos > P - p.window || pos < p.n_sink))) sr[i] = 0xFF800000u;   // -infinity
-              }
+              for (int c = 0; c < kHalves; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const int pos = pos0 + 64 * c + 32 * half + i;
+                  if (!(pos <= P && (pos > P - p.window || pos < p.n_sink))) sr[c][i] = 0xFF800000u;   // -infinity
+                }
             }
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < kC; i += 8)
+            for (int c = 0; c < kHalves; ++c)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) m4[e] = max3_f32(m4[e], __uint_as_float(sr[i + e]), __uint_as_float(sr[i + 4 + e]));
+              for (int i = 0; i < 32; i += 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m4[e] = max3_f32(m4[e], __uint_as_float(sr[c][i + e]), __uint_as_float(sr[c][i + 4 + e]));
             mx = max3_f32(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
           }
           // (also: both have read their scores, so P may take their columns)
@@ -831,44 +829,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
             m_ref = mx;
             l_sum *= alpha;
           }
-          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-          const uint64_t fac2 = pair_f32(fac, fac), mu2 = pair_f32(-mu, -mu);
-          uint64_t l2[2] = {0ull, 0ull};
-          // P over the scores: a column per two positions (fp32: hi in the first half, lo in the second)
-          const float4* vn4 = reinterpret_cast<const float4*>(norms + (t & 3) * kTile);
-          uint32_t pk[kC / 2], pl[kExact ? kC / 2 : 1];
-#pragma unroll
-          for (int i = 0; i < kC / 4; ++i) {
-            const float4 v = vn4[i];
-            const uint64_t v2[2] = {pair_f32(v.x, v.y), pair_f32(v.z, v.w)};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint64_t x = fma2_f32(pair_f32(__uint_as_float(sr[4 * i + 2 * e]), __uint_as_float(sr[4 * i + 2 * e + 1])), fac2, mu2);
-              float x0, x1;
-              unpair_f32(x, x0, x1);
-              const uint64_t pr = pair_f32(fast_exp2(x0), fast_exp2(x1));   // +0 when masked
-              l2[e] = add2_f32(l2[e], pr);
-              unpair_f32(mul2_f32(pr, v2[e]), x0, x1);
-              pk[2 * i + e] = pack_half2(x0, x1);
-              if constexpr (kExact) {
-                const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&pk[2 * i + e]));
-                pl[2 * i + e] = pack_half2(x0 - hi.x, x1 - hi.y);
-              }
-            }
-          }
-          float la, lb, lc, ld;
-          unpair_f32(l2[0], la, lb);
-          unpair_f32(l2[1], lc, ld);
-          l_sum += (la + lb) + (lc + ld);
-          if constexpr (kExact) {
-            tm_st16(lane_addr + 128 * b + 16 * half, pk);
-            tm_st16(lane_addr + 128 * b + 32 + 16 * half, pl);
-          } else {
-            tm_st32(lane_addr + 128 * b + 32 * half, pk);
-          }
-          tm_wait_st();
-          // A raised reference rescales O, half of its columns by each warp, once PV(t - 1) has completed. (S(t) came
-          // after PV(t - 2), so the barrier's phase before this one is over and its parity names one phase only.)
+          // A raised reference rescales O, half of its columns by each warp, once PV(t - 1) has completed. (QK(t) was
+          // issued after PV(t - 2), so the barrier's phase before this one is over and its parity names one phase only.)
           if (j > 0 && __any_sync(0xffffffffu, raise)) {
             ok = warp_wait(bar(kRgVEmpty + ((t - 1) & 1)), ((t - 1) >> 1) & 1);
             if (!ok) continue;   // to the next meeting
@@ -883,10 +845,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
             }
             tm_wait_st();
           }
-          tc_fence_before();
-          __syncwarp();
-          // (test hook: the first P signals are withheld, so the issuer's wait for them runs out)
-          if (lane == 0 && !(p.test_withhold && t < 2)) mbar_arrive_peer(lead_bar0 + 8u * uint32_t(kRgPFull + b));
+          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+          const uint64_t fac2 = pair_f32(fac, fac), mu2 = pair_f32(-mu, -mu);
+          uint64_t l2[2] = {0ull, 0ull};
+          // P over the scores: a column per two positions (fp32: hi in the first half, lo in the second)
+#pragma unroll
+          for (int c = 0; c < kHalves; ++c) {
+            const float4* vn4 = reinterpret_cast<const float4*>(norms + (t & 3) * kTile + 64 * c);
+            uint32_t pk[16], pl[kExact ? 16 : 1];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 v = vn4[i];
+              const uint64_t v2[2] = {pair_f32(v.x, v.y), pair_f32(v.z, v.w)};
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint64_t x = fma2_f32(pair_f32(__uint_as_float(sr[c][4 * i + 2 * e]), __uint_as_float(sr[c][4 * i + 2 * e + 1])), fac2, mu2);
+                float x0, x1;
+                unpair_f32(x, x0, x1);
+                const uint64_t pr = pair_f32(fast_exp2(x0), fast_exp2(x1));   // +0 when masked
+                l2[e] = add2_f32(l2[e], pr);
+                unpair_f32(mul2_f32(pr, v2[e]), x0, x1);
+                pk[2 * i + e] = pack_half2(x0, x1);
+                if constexpr (kExact) {
+                  const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&pk[2 * i + e]));
+                  pl[2 * i + e] = pack_half2(x0 - hi.x, x1 - hi.y);
+                }
+              }
+            }
+            tm_st16(lane_addr + 128 * b + 32 * c + 16 * half, pk);
+            if constexpr (kExact) tm_st16(lane_addr + 128 * b + 32 + 16 * half, pl);
+            tm_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            // (test hook: the first P signals are withheld, so the issuer's wait for them runs out)
+            if (lane == 0 && !(p.test_withhold && t < 2)) mbar_arrive_peer(lead_bar0 + 8u * uint32_t((c == 0 ? kRgPFull : kRgPRest) + b));
+          }
+          float la, lb, lc, ld;
+          unpair_f32(l2[0], la, lb);
+          unpair_f32(l2[1], lc, ld);
+          l_sum += (la + lb) + (lc + ld);
         }
         if (left_early) break;
         // ---- the item's rows: wait for its last PV; R^T; out
@@ -921,11 +918,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
                 x[i] = k == 0 ? mul2_f32(y, f[0]) : fma2_f32(y, f[k], x[i]);
               }
           }
-          if (sp == 1) {   // O has been read: the next item's first PV may replace it
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_peer(lead_bar0 + 8u * uint32_t(kRgOFree));
-          }
+          // (the next item's first PV, which replaces O, waits for this warp's next P)
+          if (sp == 1) tc_fence_before();
           fwht32(v[0]);
           fwht32(v[1]);
           const uint64_t minus = pair_f32(-1.f, -1.f);
@@ -964,11 +958,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
           }
         }
       }
-    } else if (w == kRgKWarp || w == kRgVWarp) {
-      // =========================================================== K tiles and norms; V tiles
+    } else if (w == kRgKWarp) {
+      // =========================================================== K tiles and the values' sizes
       if (lane == 0) {
-        const bool is_v = w == kRgVWarp;
-        const int empty = is_v ? kRgVEmpty : kRgSFull, full0 = is_v ? kRgVFull : kRgKFull;
         int t = 0;
         bool ok = true;
         while (ok && walk.next(g)) {
@@ -979,51 +971,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
             // the sinks' tiles of a block reach at most its request's, or there is no gap to skip
             const int64_t srow = int64_t(rq.tile0 + (real < rq.sink_tiles ? real : real - rq.skip)) * kTile;
             const int o = t - kStages, st = t % kStages;
-            if (o >= 0 && !(ok = bounded_wait(bar(empty + (o & 1)), (o >> 1) & 1))) break;
-            const uint32_t fb = bar(full0 + st);
-            if (is_v) {
-              mbar_expect_tx(fb, Sh::kParts * Sh::kVPart);
+            if (o >= 0 && !(ok = bounded_wait(bar(kRgSFull + (o & 1)), (o >> 1) & 1))) break;
+            const uint32_t fb = bar(kRgKFull + st);
+            mbar_expect_tx(fb, Sh::kParts * Sh::kKPart);
 #pragma unroll
-              for (int x = 0; x < Sh::kParts; ++x) {
-                const uint32_t dst = sbase + Sh::kVOff + (st * Sh::kParts + x) * Sh::kVPart;
-                const int64_t row = ((x * 2 + 1) * kHkv + g.head) * p.store_rows + srow;
+            for (int x = 0; x < Sh::kParts; ++x) {
+              const uint32_t dst = sbase + Sh::kKOff + (st * Sh::kParts + x) * Sh::kKPart;
+              const int64_t row = (x * 2 * kHkv + g.head) * p.store_rows + srow + int(rank) * (kTile / 2);
 #pragma unroll
-                for (int d = 0; d < 2; ++d)
-#pragma unroll
-                  for (int y = 0; y < 2; ++y)
-                    tma_load_2d(dst + d * Sh::kVPanel + y * (kTile / 2) * 128, &kvmap, 128 * int(rank) + 64 * d, int(row + y * (kTile / 2)), fb);
-              }
-            } else {
-              mbar_expect_tx(fb, Sh::kParts * Sh::kKPart);
-#pragma unroll
-              for (int x = 0; x < Sh::kParts; ++x) {
-                const uint32_t dst = sbase + Sh::kKOff + (st * Sh::kParts + x) * Sh::kKPart;
-                const int64_t row = (x * 2 * kHkv + g.head) * p.store_rows + srow + int(rank) * (kTile / 2);
-#pragma unroll
-                for (int d = 0; d < 4; ++d) tma_load_2d(dst + d * Sh::kKPanel, &kvmap, 64 * d, int(row), fb);
-              }
-              // the values' sizes: slot t & 3 was read by tile t - 4, whose PV came before the QK just waited for
-              const uint32_t nb = bar(kRgNFull + (t & 3));
-              mbar_expect_tx(nb, kTile * 4);
-              bulk_load(sbase + Sh::kNormOff + (t & 3) * kTile * 4, p.norms + g.head * p.store_rows + srow, kTile * 4, nb);
+              for (int d = 0; d < 4; ++d) tma_load_2d(dst + d * Sh::kKPanel, &kvmap, 64 * d, int(row), fb);
             }
+            // the values' sizes: slot t & 3 was read by tile t - 4, whose PV came before the QK just waited for
+            const uint32_t nb = bar(kRgNFull + (t & 3));
+            mbar_expect_tx(nb, kTile * 4);
+            bulk_load(sbase + Sh::kNormOff + (t & 3) * kTile * 4, p.norms + g.head * p.store_rows + srow, kTile * 4, nb);
           }
         }
         if (misc[1]) {
-          for (int o = max(t - kStages, 0); o < t; ++o) drain(bar(full0 + o % kStages), (o / kStages) & 1);
-          if (!is_v)
-            for (int o = max(t - kRgNormSlots, 0); o < t; ++o) drain(bar(kRgNFull + (o & 3)), (o >> 2) & 1);
+          for (int o = max(t - kStages, 0); o < t; ++o) drain(bar(kRgKFull + o % kStages), (o / kStages) & 1);
+          for (int o = max(t - kRgNormSlots, 0); o < t; ++o) drain(bar(kRgNFull + (o & 3)), (o >> 2) & 1);
         }
       }
-    } else if (w == kRgQWarp) {
-      // =========================================================== Q rows and the item's record
-      int s = 0;
+    } else if (w == kRgVWarp) {
+      // =========================================================== Q rows and the item's record, then its V tiles
+      int s = 0, t = 0;
+      bool ok = true;
       while (walk.next(g)) {
         const RgReq rq = p.req[p.blk_req[g.blk]];
         const int rb = g.blk - rq.blk0, n_rows = min(256, 6 * rq.n_new - 256 * rb);
         const int64_t row = int64_t(g.head) * kGroup * p.n_tok + int64_t(rq.row0) * kGroup + 256 * rb;
-        // Slot s & 3 held item s - 4. Here item s - 2's last QK has run; it was issued after item s - 3's PV, which
-        // takes that item's P: the softmax has read the records up to s - 3.
+        // Slot s & 3 held item s - 4. Here item s - 2's last QK has run, and so item s - 4's last PV, which takes
+        // that item's P: the softmax has read its record.
         float* const fac = reinterpret_cast<float*>(smem + Sh::kFacOff) + (s & 3) * kPfRows;
 #pragma unroll
         for (int i = 0; i < kPfRows / 32; ++i) fac[32 * i + lane] = p.qfac[row + min(int(rank) * kPfRows + 32 * i + lane, n_rows - 1)];
@@ -1033,40 +1011,86 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
               RgItem{g.n, g.tile, span.sinks, span.skip, rq.first, 256 * rb, n_rows, g.head, rq.row0, g.part, {0, 0}};
         }
         __syncwarp();
-        bool ok = true;
-        if (lane == 0 && s > 0) ok = bounded_wait(bar(kRgQFree), (s - 1) & 1);   // the last item's last QK has run
-        if (!__all_sync(0xffffffffu, ok)) break;
         if (lane == 0) {
-          mbar_expect_tx(bar(kRgQFull), Sh::kParts * Sh::kQPart);
+          if (s > 0) ok = bounded_wait(bar(kRgQFree), (s - 1) & 1);   // the last item's last QK has run
+          if (ok) {
+            mbar_expect_tx(bar(kRgQFull), Sh::kParts * Sh::kQPart);
 #pragma unroll
-          for (int x = 0; x < Sh::kParts; ++x)
+            for (int x = 0; x < Sh::kParts; ++x)
 #pragma unroll
-            for (int d = 0; d < 4; ++d)
-              tma_load_2d(sbase + x * Sh::kQPart + d * Sh::kQPanel, &qmap, 64 * d, int(x * int64_t(kHq) * p.n_tok + row + int(rank) * kPfRows),
-                          bar(kRgQFull));
+              for (int d = 0; d < 4; ++d)
+                tma_load_2d(sbase + x * Sh::kQPart + d * Sh::kQPanel, &qmap, 64 * d, int(x * int64_t(kHq) * p.n_tok + row + int(rank) * kPfRows),
+                            bar(kRgQFull));
+            ++s;
+          }
+          const RgSpan span = rg_block_span<kTile>(p, rq, rb);
+          for (int j = 0; ok && j < g.n; ++j) {
+            const int at = g.tile + j, real = at < span.sinks ? at : at + span.skip;
+            const int64_t srow = int64_t(rq.tile0 + (real < rq.sink_tiles ? real : real - rq.skip)) * kTile;
+            const int o = t - kStages, st = t % kStages;
+            if (o >= 0 && !(ok = bounded_wait(bar(kRgVEmpty + (o & 1)), (o >> 1) & 1))) break;
+            const uint32_t fb = bar(kRgVFull + st);
+            mbar_expect_tx(fb, Sh::kParts * Sh::kVPart);
+#pragma unroll
+            for (int x = 0; x < Sh::kParts; ++x) {
+              const uint32_t dst = sbase + Sh::kVOff + (st * Sh::kParts + x) * Sh::kVPart;
+              const int64_t vrow = ((x * 2 + 1) * kHkv + g.head) * p.store_rows + srow;
+#pragma unroll
+              for (int d = 0; d < 2; ++d)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                  tma_load_2d(dst + d * Sh::kVPanel + y * (kTile / 2) * 128, &kvmap, 128 * int(rank) + 64 * d, int(vrow + y * (kTile / 2)), fb);
+            }
+            ++t;
+          }
         }
-        ++s;
+        s = __shfl_sync(0xffffffffu, s, 0);
+        if (!__all_sync(0xffffffffu, ok)) break;
       }
-      if (lane == 0 && misc[1] && s > 0) drain(bar(kRgQFull), (s - 1) & 1);
+      if (lane == 0 && misc[1]) {
+        if (s > 0) drain(bar(kRgQFull), (s - 1) & 1);
+        for (int o = max(t - kStages, 0); o < t; ++o) drain(bar(kRgVFull + o % kStages), (o / kStages) & 1);
+      }
     } else if (rank == 1) {
       // =========================================================== rank 1: its copies have landed
+      if (lane == 0) {
+        const bool is_k = w == kRgMmaWarp;
+        const int full = is_k ? kRgKFull : kRgVFull, peer = is_k ? kRgKPeer : kRgVPeer;
+        int t = 0, s = 0;
+        bool ok = true;
+        while (ok && walk.next(g)) {
+          if (is_k) {
+            if (!(ok = bounded_wait(bar(kRgQFull), s & 1))) break;
+            mbar_arrive_peer(lead_bar0 + 8u * uint32_t(kRgQPeer));
+            ++s;
+          }
+          for (int j = 0; j < g.n; ++j, ++t) {
+            const int st = t % kStages;
+            if (!(ok = bounded_wait(bar(full + st), (t / kStages) & 1))) break;
+            mbar_arrive_peer(lead_bar0 + 8u * uint32_t(peer + st));
+          }
+        }
+      }
+    } else if (w != kRgMmaWarp) {
+      // =========================================================== rank 0: both CTAs' copies -> one barrier a burst
       if (lane == 0) {
         int t = 0, s = 0;
         bool ok = true;
         while (ok && walk.next(g)) {
-          if (!(ok = bounded_wait(bar(kRgQFull), s & 1))) break;
-          mbar_arrive_peer(lead_bar0 + 8u * uint32_t(kRgQPeer));
+          if (!(ok = bounded_wait(bar(kRgQFull), s & 1) && bounded_wait(bar(kRgQPeer), s & 1))) break;
           ++s;
-          for (int j = 0; ok && j <= g.n; ++j) {   // in the order in which rank 0 waits for them
+          for (int j = 0; j <= g.n; ++j) {   // in the order in which the issuer needs them
             if (j < g.n) {
               const int u = t + j, st = u % kStages;
-              if (!(ok = bounded_wait(bar(kRgKFull + st), (u / kStages) & 1))) break;
-              mbar_arrive_peer(lead_bar0 + 8u * uint32_t(kRgKPeer + st));
+              const uint32_t par = (u / kStages) & 1;
+              if (!(ok = bounded_wait(bar(kRgKFull + st), par) && bounded_wait(bar(kRgKPeer + st), par))) break;
+              mbar_arrive_local(bar(kRgKReady + (u & 1)));
             }
             if (j > 0) {
               const int u = t + j - 1, st = u % kStages;
-              if (!(ok = bounded_wait(bar(kRgVFull + st), (u / kStages) & 1))) break;
-              mbar_arrive_peer(lead_bar0 + 8u * uint32_t(kRgVPeer + st));
+              const uint32_t par = (u / kStages) & 1;
+              if (!(ok = bounded_wait(bar(kRgVFull + st), par) && bounded_wait(bar(kRgVPeer + st), par))) break;
+              mbar_arrive_local(bar(kRgPFull + (u & 1)));
             }
           }
           t += g.n;
@@ -1074,27 +1098,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
       }
     } else {
       // =========================================================== rank 0: MMA issuer (one thread)
-      // A look at a barrier queues behind the products issued before it and takes 250 cycles and more, and the
-      // tensor pipe runs dry meanwhile. So the next burst's barriers are looked at in the middle of this one, the
-      // answers are taken at its end, and only a barrier not yet seen complete is waited for.
       if (lane == 0) {
         constexpr uint32_t idesc_qk = tc_idesc(2 * kPfRows, kTile, 0);
         constexpr uint32_t idesc_pv = tc_idesc(2 * kPfRows, kD, 1);
         const uint64_t q0 = tc_sdesc(sbase, 16, 1024);
-        int t = 0, s = 0;
+        int t = 0;
         bool ok = true;
         while (ok && walk.next(g)) {
-          if (!(ok = bounded_wait(bar(kRgQFull), s & 1) && bounded_wait(bar(kRgQPeer), s & 1))) break;
-          ++s;
-          uint32_t k_seen = 0;
           for (int j = 0; j <= g.n; ++j) {
-            const int up = t + j - 1, vst = up & (kStages - 1);   // tile of this round's PV
-            const uint32_t vpar = (up / kStages) & 1, ppar = (up >> 1) & 1;
-            uint32_t pv_seen = 0;
             if (j < g.n) {   // S[u & 1] = Q K^T
-              const int u = t + j, st = u & (kStages - 1);
-              const uint32_t par = (u / kStages) & 1;
-              if (!k_seen && !(ok = bounded_wait(bar(kRgKFull + st), par) && bounded_wait(bar(kRgKPeer + st), par))) break;
+              const int u = t + j, st = u % kStages;
+              if (!(ok = bounded_wait(bar(kRgKReady + (u & 1)), (u >> 1) & 1))) break;
               tc_fence_after();
               const uint32_t s_t = tmem + 128 * (u & 1);
 #pragma unroll
@@ -1102,43 +1116,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
                 const uint64_t qx = q0 + (x == 1 ? (Sh::kQPart >> 4) : 0);
                 const uint64_t kx = tc_sdesc(sbase + Sh::kKOff + (st * Sh::kParts + (x == 2 ? 1 : 0)) * Sh::kKPart, 16, 1024);
 #pragma unroll
-                for (int kk = 0; kk < 16; ++kk) {
+                for (int kk = 0; kk < 16; ++kk)
                   tc2_mma_ss(s_t, qx + (((kk >> 2) * Sh::kQPanel + (kk & 3) * 32) >> 4), kx + (((kk >> 2) * Sh::kKPanel + (kk & 3) * 32) >> 4),
                              idesc_qk, (x > 0 || kk > 0) ? 1u : 0u);
-                  if (x == (kExact ? 2 : 0) && kk == 11)
-                    pv_seen = mbar_look(bar(kRgVFull + vst), vpar) & mbar_look(bar(kRgVPeer + vst), vpar) & mbar_look(bar(kRgPFull + (up & 1)), ppar) &
-                              (j > 0 ? 1u : 0u);
-                }
               }
               tc2_commit_both(bar(kRgSFull + (u & 1)));
               if (j == g.n - 1) tc2_commit_both(bar(kRgQFree));
             }
-            k_seen = 0;
             if (j > 0) {   // O += P V of tile j - 1
-              if (!pv_seen && !(ok = bounded_wait(bar(kRgVFull + vst), vpar) && bounded_wait(bar(kRgVPeer + vst), vpar) &&
-                                     bounded_wait(bar(kRgPFull + (up & 1)), ppar)))
-                break;
-              if (j == 1 && s > 1 && !(ok = bounded_wait(bar(kRgOFree), s & 1))) break;   // the last item's rows have been read
-              tc_fence_after();
-              const uint32_t p_t = tmem + 128 * (up & 1);
-              const int un = t + j + 1, nst = un & (kStages - 1);   // the next round's QK
-              const uint32_t npar = (un / kStages) & 1;
+              const int u = t + j - 1, st = u % kStages;
+              const uint32_t p_t = tmem + 128 * (u & 1);
 #pragma unroll
-              for (int x = 0; x < (kExact ? 3 : 1); ++x) {   // Ph Vh, Pl Vh, Ph Vl
-                const uint64_t vx = tc_sdesc(sbase + Sh::kVOff + (vst * Sh::kParts + (x == 2 ? 1 : 0)) * Sh::kVPart, Sh::kVPanel, 1024);
+              for (int c = 0; c < (kExact ? 1 : 2); ++c) {   // 64 positions; the first P also says that O may be written
+                if (!(ok = bounded_wait(bar((c == 0 ? kRgPFull : kRgPRest) + (u & 1)), (u >> 1) & 1))) break;
+                tc_fence_after();
 #pragma unroll
-                for (int ks = 0; ks < kTile / 16; ++ks) {
-                  tc2_mma_ts(tmem + kTmO, p_t + (x == 1 ? 32 : 0) + 8 * ks, vx + ((ks * 16 * 128) >> 4), idesc_pv, (j > 1 || x > 0 || ks > 0) ? 1u : 0u);
-                  if (x == (kExact ? 2 : 0) && ks == kTile / 32)
-                    k_seen = mbar_look(bar(kRgKFull + nst), npar) & mbar_look(bar(kRgKPeer + nst), npar) & (j + 1 < g.n ? 1u : 0u);
+                for (int x = 0; x < (kExact ? 3 : 1); ++x) {   // Ph Vh, Pl Vh, Ph Vl
+                  const uint64_t vx = tc_sdesc(sbase + Sh::kVOff + (st * Sh::kParts + (x == 2 ? 1 : 0)) * Sh::kVPart, Sh::kVPanel, 1024);
+#pragma unroll
+                  for (int ks = 4 * c; ks < 4 * c + 4; ++ks)
+                    tc2_mma_ts(tmem + kTmO, p_t + (x == 1 ? 32 : 0) + 8 * ks, vx + ((ks * 16 * 128) >> 4), idesc_pv,
+                               (j > 1 || x > 0 || ks > 0) ? 1u : 0u);
                 }
               }
-              tc2_commit_both(bar(kRgVEmpty + (up & 1)));
+              if (!ok) break;
+              tc2_commit_both(bar(kRgVEmpty + (u & 1)));
             }
           }
           t += g.n;
         }
-        // every MMA that this thread issued has completed before TMEM is released
+        // every product that this thread issued has completed before TMEM is released
         tc2_commit_own(bar(kRgDrain));
         drain(bar(kRgDrain), 0);
       }
