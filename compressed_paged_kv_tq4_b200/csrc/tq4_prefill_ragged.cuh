@@ -59,6 +59,9 @@ constexpr int kRgSoftWarps = 8, kRgKWarp = 8, kRgMmaWarp = 9, kRgVWarp = 10;   /
 constexpr int kRgThreads = 32 * 12;
 constexpr int kRgNormSlots = 4;
 constexpr int kRgMinTiles = 256;      // positions: a pair's share is at least this many (a few tiles)
+// An item's queries and epilogue cost a pair about four tiles' time (12,000 cycles), which its share has to
+// count where a pair gets many tiles: 31 short items beside 2 long ones took 880,000 cycles against 580,000.
+constexpr int kRgItemCost = 4, kRgItemCostFrom = 16;   // tiles; from so many tiles a pair
 template <bool kExact>
 struct RgShape {
   static constexpr int kTile = kExact ? 64 : 128;            // positions per tile
@@ -205,50 +208,126 @@ __device__ __forceinline__ RgSpan rg_block_span(const RaggedParams& p, const RgR
 
 // --------------------------------------------------------------------------
 // prep. Every CTA scans the requests (as plan_step does); CTA 0 then lays out the work, the
-// others make rows: units of 32 positions of one (row tile, KV head), keys and values, and of one
+// others make rows, a warp at a time: four positions of one KV head, keys and values, or four of a
 // token's queries.
 // --------------------------------------------------------------------------
 constexpr int kRgPrepThreads = 256;
 
-// f16 rows of one vector held as 8 coordinates a lane (already times `down`)
-template <bool kExact>
-__device__ __forceinline__ void rg_store_row(__half* dst, int64_t part_stride, const float v[8]) {
-  const int lane = threadIdx.x & 31;
-  uint32_t hi[4];
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pair_f32(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpair_f32(uint64_t d, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d)); }
+__device__ __forceinline__ uint64_t fma2_f32(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2_f32(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2_f32(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// Eight lanes hold a vector, four vectors a warp: lane 8 x + i has dims 64 c + 8 i .. + 7 of vector x in
+// block c, as pairs of floats. So 16-byte accesses of eight lanes are contiguous, five of the transform's
+// eight levels stay in registers and three cross lanes (against five with a vector across the warp: half
+// the instructions a vector).
+struct RgVec { uint64_t v[4][4]; };
+struct RgMask { uint32_t m[4][4]; };   // the signs of this lane's dims, as bits of packed bf16 pairs
+__device__ __forceinline__ void rg_mask(const Signs& s, RgMask& k) {
+  const int i = threadIdx.x & 7;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) hi[i] = pack_half2(v[2 * i], v[2 * i + 1]);
-  *reinterpret_cast<uint4*>(dst + lane * 8) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-  if constexpr (kExact) {
-    uint32_t lo[4];
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t bits = (i < 4 ? s.bits[2 * c] : s.bits[2 * c + 1]) >> (8 * (i & 3));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
-      lo[i] = pack_half2(v[2 * i] - h.x, v[2 * i + 1] - h.y);
-    }
-    *reinterpret_cast<uint4*>(dst + part_stride + lane * 8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    for (int x = 0; x < 4; ++x) k.m[c][x] = ((bits >> (2 * x)) & 1u) << 15 | ((bits >> (2 * x + 1)) & 1u) << 31;
   }
 }
-// R x * 16 of a bf16 vector in v; returns the largest magnitude's bits (infinities and NaN above every number)
-__device__ __forceinline__ uint32_t rg_rotate(const uint4 raw, uint32_t sb, float v[8]) {
-  const uint32_t ww[4] = {raw.x, raw.y, raw.z, raw.w};
+__device__ __forceinline__ void butterfly2(uint64_t& a, uint64_t& b, uint64_t minus) {
+  const uint64_t x = a, y = b;
+  a = add2_f32(x, y);
+  b = fma2_f32(y, minus, x);
+}
+// R x * 16 of bf16 vectors; returns each one's largest magnitude as bits (infinities and NaN above every number)
+__device__ __forceinline__ uint32_t rg_rotate4(const uint4 (&raw)[4], const RgMask& k, RgVec& r) {
+  const uint64_t minus = pair_f32(-1.f, -1.f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = apply_sign(__uint_as_float(ww[i] << 16), sb, 2 * i);
-    v[2 * i + 1] = apply_sign(__uint_as_float(ww[i] & 0xFFFF0000u), sb, 2 * i + 1);
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t w[4] = {raw[c].x ^ k.m[c][0], raw[c].y ^ k.m[c][1], raw[c].z ^ k.m[c][2], raw[c].w ^ k.m[c][3]};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float a = __uint_as_float(w[x] << 16), b = __uint_as_float(w[x] & 0xFFFF0000u);
+      r.v[c][x] = pair_f32(a + b, a - b);
+    }
+    butterfly2(r.v[c][0], r.v[c][1], minus);
+    butterfly2(r.v[c][2], r.v[c][3], minus);
+    butterfly2(r.v[c][0], r.v[c][2], minus);
+    butterfly2(r.v[c][1], r.v[c][3], minus);
   }
-  warp_fwht256(v);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    butterfly2(r.v[0][x], r.v[1][x], minus);
+    butterfly2(r.v[2][x], r.v[3][x], minus);
+    butterfly2(r.v[0][x], r.v[2][x], minus);
+    butterfly2(r.v[1][x], r.v[3][x], minus);
+  }
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  return __reduce_max_sync(0xffffffffu, top);
-}
-// v brought to [0.5, 1) by 2^-e (zeros stay); returns 2^e
-__device__ __forceinline__ float rg_scale(uint32_t top, float v[8]) {
-  const int e = min(max(int(top >> 23) - 126, -100), 126);
-  const float down = __uint_as_float(uint32_t(127 - e) << 23);
+  for (int m = 1; m < 8; m <<= 1) {
+    const float own = (threadIdx.x & m) ? -1.f : 1.f;
+    const uint64_t own2 = pair_f32(own, own);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] *= down;
-  return __uint_as_float(uint32_t(127 + e) << 23);
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        float a, b;
+        unpair_f32(r.v[c][x], a, b);
+        r.v[c][x] = fma2_f32(own2, r.v[c][x], pair_f32(__shfl_xor_sync(0xffffffffu, a, m), __shfl_xor_sync(0xffffffffu, b, m)));
+      }
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      float a, b;
+      unpair_f32(r.v[c][x], a, b);
+      top = max(top, max(__float_as_uint(a) & 0x7FFFFFFFu, __float_as_uint(b) & 0x7FFFFFFFu));
+    }
+#pragma unroll
+  for (int m = 1; m < 8; m <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+  return top;
+}
+// 2^e with top * 2^-e in [0.5, 1) (for a zero 2^-100)
+__device__ __forceinline__ int rg_exponent(uint32_t top) { return min(max(int(top >> 23) - 126, -100), 126); }
+__device__ __forceinline__ float rg_pow2(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
+// times f, as f16 hi (and lo) to this vector's row
+template <bool kExact>
+__device__ __forceinline__ void rg_store4(__half* row, int64_t part_stride, const RgVec& r, float f) {
+  const uint64_t f2 = pair_f32(f, f);
+  __half* const dst = row + 8 * (threadIdx.x & 7);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      float a, b;
+      unpair_f32(mul2_f32(r.v[c][x], f2), a, b);
+      hi[x] = pack_half2(a, b);
+      if constexpr (kExact) {
+        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[x]));
+        lo[x] = pack_half2(a - h.x, b - h.y);
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + 64 * c) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if constexpr (kExact) *reinterpret_cast<uint4*>(dst + part_stride + 64 * c) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
 }
 // below 2^15 * 16: a rotated coordinate (times 16) up to this fits an f16, and so does a value's size times
 // the largest weight, 2^4 / 16
@@ -376,157 +455,177 @@ __global__ void __launch_bounds__(kRgPrepThreads) ragged_prep_kernel(const Ragge
     }
     const int64_t per_head = carry[0], all = per_head * kHkv;
     constexpr int64_t kMin = kRgMinTiles / kTile;
-    const int pairs = int(min(int64_t(p.max_pairs), all > 0 ? max(all / kMin, int64_t(1)) : int64_t(0)));
+    // The line is cut by cost, tiles and items' overhead; a cut inside an item's overhead lies before its first
+    // tile. Shares of at least the overhead and two tiles are never empty.
+    const int64_t extra = all >= int64_t(p.max_pairs) * kRgItemCostFrom ? kRgItemCost : 0;
+    const int64_t cost_head = per_head + extra * s_blocks, cost = cost_head * kHkv;
+    const int pairs = int(min(int64_t(p.max_pairs), all > 0 ? max(cost / (kMin + extra), int64_t(1)) : int64_t(0)));
     if (tid == 0) {
       p.blk_cum[s_blocks] = per_head;
       *p.head = RgHead{s_blocks, s_tiles, pairs, 0};
     }
     __syncthreads();
     for (int s = tid; s < pairs; s += kRgPrepThreads) {
-      const int64_t g = int64_t(s) * all / pairs, head = g / per_head, at = g - head * per_head;
-      const int blk = rg_last_at_most<int64_t>(p.blk_cum, s_blocks, at);
-      p.starts[s] = RgStart{int32_t(head), blk, int32_t(at - p.blk_cum[blk]), 0};
+      const int64_t g = int64_t(s) * cost / pairs, head = g / cost_head, at = g - head * cost_head;
+      int lo = 0, hi = s_blocks - 1;   // the last block whose cost begins at or before `at`
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.blk_cum[mid] + extra * mid <= at) lo = mid;
+        else hi = mid - 1;
+      }
+      p.starts[s] = RgStart{int32_t(head), lo, int32_t(max(at - p.blk_cum[lo] - extra * (lo + 1), int64_t(0))), 0};
     }
     return;
   }
 
   // ---- rows
-  const uint32_t sb = lane_sign_bits(p.signs);
-  constexpr int kQuarters = kTile / 32;
-  const int64_t kv_units = int64_t(s_tiles) * kHkv * kQuarters;
+  RgMask mask;
+  rg_mask(p.signs, mask);
+  const int sub = lane >> 3;            // this lane's vector of the four
+  const int at8 = 8 * (lane & 7);       // and its first dim of each block of 64
+  constexpr int kFours = kTile / 4;
+  const int64_t kv_units = int64_t(s_tiles) * kHkv * kFours;
   const int32_t live = int32_t(min(max(int64_t(cu0) + carry[0], int64_t(0)), int64_t(p.n_tok)));   // rows of the last request end here
   const int64_t q_part = int64_t(kHq) * p.n_tok * kD, kv_part = int64_t(2) * kHkv * p.store_rows * kD;
-  for (int64_t u = int64_t(blockIdx.x) - 1; u < kv_units + live; u += int64_t(gridDim.x) - 1) {
-    if (u >= kv_units) {   // one token's 24 queries
-      const int tok = int(u - kv_units);
+  constexpr int kWarps = kRgPrepThreads / 32;
+  // (consecutive units go to different CTAs, so that a small call spreads out)
+  for (int64_t u = int64_t(w) * (int64_t(gridDim.x) - 1) + int64_t(blockIdx.x) - 1; u < kv_units + int64_t(live) * (kHq / 4);
+       u += kWarps * (int64_t(gridDim.x) - 1)) {
+    uint4 raw[4];
+    RgVec vec;
+    if (u >= kv_units) {   // four of a token's queries
+      const int tok = int((u - kv_units) / (kHq / 4)), hq = 4 * int((u - kv_units) % (kHq / 4)) + sub, h = hq / kGroup;
       if (tok < cu0) continue;
+      const int64_t off = (int64_t(tok) * kHq + hq) * kD + at8;
       const int r = rg_last_at_most<int32_t>(row0_s, p.n_req, tok);
       const int32_t T = p.seq_lens[r], a = p.cu[r], b = p.cu[r + 1];
       const bool work = a >= 0 && a == row0_s[r] && b <= p.n_tok && tok >= a && tok < b && T > 0 &&
                         int64_t(T) <= int64_t(p.max_pages) * kPage && T >= b - a;
+      if (!work) {   // a refused request: zeros
+        const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int x = 0; x < kHq / 8; ++x) {
-        const int hq = w + 8 * x, h = hq / kGroup;
-        if (!work) {   // a refused request: zeros
-          const int64_t off = (int64_t(tok) * kHq + hq) * kD + lane * 8;
-          const uint4 z = make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < 4; ++c) {
           if (p.out_dtype == TQ4_DTYPE_F32) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(p.out) + off);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(p.out) + off + 64 * c);
             dst[0] = z;
             dst[1] = z;
           } else {
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + off) = z;
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + off + 64 * c) = z;
           }
-          continue;
         }
-        float v[8];
-        const uint32_t top = rg_rotate(__ldg(reinterpret_cast<const uint4*>(p.q + (int64_t(tok) * kHq + hq) * kD + lane * 8)), sb, v);
-        const float up = top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : rg_scale(top, v);   // (a row with a NaN is its own only)
-        const int64_t row = int64_t(h) * kGroup * p.n_tok + int64_t(tok) * kGroup + (hq - h * kGroup);
-        // the scores' factor is kept positive (the scale's sign goes into the row) and above zero,
-        // so that a masked -infinity stays one
-        const float sgn = p.scale > 0.f ? 1.f : p.scale < 0.f ? -1.f : 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= sgn;
-        rg_store_row<kExact>(p.qr + row * kD, q_part, v);
-        // (fmaxf would drop the NaN of a row that holds one)
-        const float fac = up * (fabsf(p.scale) * 0.0625f * kLog2e);
-        if (lane == 0) p.qfac[row] = fac < 1.17549435e-38f ? 1.17549435e-38f : fac;
+        continue;
       }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) raw[c] = __ldg(reinterpret_cast<const uint4*>(p.q + off + 64 * c));
+      const uint32_t top = rg_rotate4(raw, mask, vec);
+      const int e = rg_exponent(top);
+      const int64_t row = int64_t(h) * kGroup * p.n_tok + int64_t(tok) * kGroup + (hq - h * kGroup);
+      // the scores' factor is kept positive (the scale's sign goes into the row) and above zero, so that a
+      // masked -infinity stays one
+      rg_store4<kExact>(p.qr + row * kD, q_part, vec, p.scale > 0.f ? rg_pow2(-e) : p.scale < 0.f ? -rg_pow2(-e) : 0.f);
+      // (a row with an infinity or a NaN is its own only; fmaxf would drop the NaN)
+      const float fac = top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : rg_pow2(e) * (fabsf(p.scale) * 0.0625f * kLog2e);
+      if ((lane & 7) == 0) p.qfac[row] = fac < 1.17549435e-38f ? 1.17549435e-38f : fac;
       continue;
     }
-    // 32 positions of a row tile, one KV head: four a warp, keys and values together
-    const int part = int(u % kQuarters), h = int((u / kQuarters) & 3), st = int(u / (kQuarters * kHkv));
+    // four positions of a row tile, one KV head, keys and values together
+    const int four = int(u % kFours), h = int((u / kFours) & 3), st = int(u / (kFours * kHkv));
     const int r = rg_last_at_most<int32_t>(tile0_s, p.n_req, st);   // requests without tiles share their next's tile0
     const int32_t T = p.seq_lens[r], row0 = p.cu[r], first = T - (p.cu[r + 1] - row0);
     const int32_t lo = max(0, first - p.window + 1);
     const RgSpan s = rg_span<kTile>(lo, T - 1, p.n_sink);
     const int local = st - tile0_s[r];
-    const int32_t pos0 = (local < s.sinks ? local : local + s.skip) * kTile + 32 * part + 4 * w;   // this warp's four
-    const int64_t srow0 = int64_t(st) * kTile + 32 * part + 4 * w;
-    const int32_t page = pos0 < first ? __ldg(p.tables + int64_t(r) * p.max_pages + (pos0 >> 8)) : -1;   // a tile lies in one page
-    const bool page_ok = page >= 0 && page < p.num_pages;
-    const uint8_t* pg = p.pool + int64_t(page_ok ? page : 0) * kPageBytes;
+    const int32_t pos0 = (local < s.sinks ? local : local + s.skip) * kTile + 4 * four;   // this warp's four
+    const int64_t srow0 = int64_t(st) * kTile + 4 * four;
     __half* const k0 = p.rows + (int64_t(h) * p.store_rows + srow0) * kD;
     __half* const v0 = p.rows + (int64_t(kHkv + h) * p.store_rows + srow0) * kD;
-    float size = 0.f;   // lane i < 4: that of value i
-    bool bad_page = false;
-    uint4 raw_k[4], raw_v[4];   // a chunk vector's eight elements a lane; a cached one's word in .x, its norm in .y
+    if (pos0 + 3 >= first && pos0 < T) {   // the chunk's own are among them: eight lanes each
+      const int32_t pos = pos0 + sub;
+      const bool mine = pos >= first && pos < T;
+      const int64_t off = (int64_t(row0 + pos - first) * kHkv + h) * kD + at8;
+      uint4 raw_v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int32_t pos = pos0 + i;
-      raw_k[i] = raw_v[i] = make_uint4(0, 0, 0, 0);
-      if (pos >= first && pos < T) {
-        const int64_t off = (int64_t(row0 + pos - first) * kHkv + h) * kD + lane * 8;
-        raw_k[i] = __ldg(reinterpret_cast<const uint4*>(p.k + off));
-        raw_v[i] = __ldg(reinterpret_cast<const uint4*>(p.v + off));
-      } else if (pos < first && (pos >= lo || pos < p.n_sink)) {
-        bad_page |= !page_ok;
-        if (page_ok) {
-          const int slot = h * kPage + (pos & (kPage - 1));
-          raw_k[i].x = ldg32(pg + kKWords + int64_t(slot) * 128 + lane * 4);
-          raw_v[i].x = ldg32(pg + kVWords + int64_t(slot) * 128 + lane * 4);
-          raw_k[i].y = __ldg(reinterpret_cast<const unsigned short*>(pg + kKNorms + slot * 2));
-          raw_v[i].y = __ldg(reinterpret_cast<const unsigned short*>(pg + kVNorms + slot * 2));
+      for (int c = 0; c < 4; ++c) {
+        raw[c] = mine ? __ldg(reinterpret_cast<const uint4*>(p.k + off + 64 * c)) : make_uint4(0, 0, 0, 0);
+        raw_v[c] = mine ? __ldg(reinterpret_cast<const uint4*>(p.v + off + 64 * c)) : make_uint4(0, 0, 0, 0);
+      }
+      RgVec vv;
+      const uint32_t ktop = rg_rotate4(raw, mask, vec), vtop = rg_rotate4(raw_v, mask, vv);
+      const bool fits = ktop <= kRgTop && vtop <= kRgTop;
+      const int e = rg_exponent(vtop);
+      if (mine) {
+        if (!fits) {   // zeros and a NaN key
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              vec.v[c][x] = 0x7FC000007FC00000ull;
+              vv.v[c][x] = 0ull;
+            }
         }
-      }   // else nobody sees it: zeros
+        rg_store4<kExact>(k0 + sub * kD, kv_part, vec, 0.0625f);
+        rg_store4<kExact>(v0 + sub * kD, kv_part, vv, rg_pow2(-e));
+        if ((lane & 7) == 0) p.norms[int64_t(h) * p.store_rows + srow0 + sub] = fits ? 0.0625f * Sh::kPScale * rg_pow2(e) : 0.f;
+      }
     }
+    if (pos0 < first || pos0 + 3 >= T) {   // cached ones, and rows that nobody sees (zeros)
+      const int32_t page = pos0 < first ? __ldg(p.tables + int64_t(r) * p.max_pages + (pos0 >> 8)) : -1;   // a tile lies in one page
+      const bool page_ok = page >= 0 && page < p.num_pages;
+      const uint8_t* pg = p.pool + int64_t(page_ok ? page : 0) * kPageBytes;
+      uint32_t wk[4], wv[4];
+      uint16_t nk[4], nv[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int32_t pos = pos0 + i;
-      float mine;
-      if (pos >= first && pos < T) {   // the chunk's own
-        float a[8], b[8];
-        const uint32_t ktop = rg_rotate(raw_k[i], sb, a), vtop = rg_rotate(raw_v[i], sb, b);
-        const bool fits = ktop <= kRgTop && vtop <= kRgTop;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          a[x] = fits ? a[x] * 0.0625f : __uint_as_float(0x7FC00000u);
-          b[x] = fits ? b[x] : 0.f;
+      for (int i = 0; i < 4; ++i) {
+        const int32_t pos = pos0 + i;
+        const bool seen = pos < first && (pos >= lo || pos < p.n_sink);
+        wk[i] = wv[i] = 0;
+        nk[i] = nv[i] = 0;
+        if (seen && page_ok) {
+          const int slot = h * kPage + (pos & (kPage - 1));
+          wk[i] = ldg32(pg + kKWords + int64_t(slot) * 128 + lane * 4);
+          wv[i] = ldg32(pg + kVWords + int64_t(slot) * 128 + lane * 4);
+          nk[i] = __ldg(reinterpret_cast<const unsigned short*>(pg + kKNorms + slot * 2));
+          nv[i] = __ldg(reinterpret_cast<const unsigned short*>(pg + kVNorms + slot * 2));
+        } else if (seen && lane == 0) {
+          record_error(p.status, TQ4_ERR_PAGE_RANGE);
         }
-        mine = 0.0625f * Sh::kPScale * rg_scale(fits ? vtop : 0u, b);
-        rg_store_row<kExact>(k0 + i * kD, kv_part, a);
-        rg_store_row<kExact>(v0 + i * kD, kv_part, b);
-      } else {
-        const float kn = __half2float(__ushort_as_half(uint16_t(raw_k[i].y))), vn = __half2float(__ushort_as_half(uint16_t(raw_v[i].y)));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int32_t pos = pos0 + i;
+        if (pos >= first && pos < T) continue;
+        const float kn = __half2float(__ushort_as_half(nk[i])), vn = __half2float(__ushort_as_half(nv[i]));
         const bool fits = fabsf(vn) <= 65504.f;   // false: an infinity or a NaN
-        const uint32_t wk = raw_k[i].x, wv = raw_v[i].x;
         const int copy = lane & 7;
-        const __half2 n2 = fits ? __half2half2(__ushort_as_half(uint16_t(raw_k[i].y))) : __half2half2(__ushort_as_half(0x7E00));
-        uint32_t kk[4], vv[4];
+        const __half2 n2 = __half2half2(__ushort_as_half(fits ? nk[i] : uint16_t(0x7E00)));
+        uint32_t kk[4], vv[4], kl[4], vl[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const uint32_t c = pair_s[(wk >> (8 * x)) & 255u][copy];
-          vv[x] = pair_s[(wv >> (8 * x)) & 255u][copy];
-          if constexpr (!kExact) {
+          const uint32_t bk = (wk[i] >> (8 * x)) & 255u, bv = (wv[i] >> (8 * x)) & 255u;
+          const uint32_t c = pair_s[bk][copy];
+          vv[x] = pair_s[bv][copy];
+          if constexpr (kExact) {
+            const uint32_t cl = res_s[bk][copy];
+            const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&c)), lf = __half22float2(*reinterpret_cast<const __half2*>(&cl));
+            const float n = fits ? kn : __uint_as_float(0x7FC00000u), a = (hf.x + lf.x) * n, b = (hf.y + lf.y) * n;
+            kk[x] = pack_half2(a, b);
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&kk[x]));
+            kl[x] = pack_half2(a - back.x, b - back.y);
+            vl[x] = res_s[bv][copy];
+          } else {
             const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&c), n2);
             kk[x] = *reinterpret_cast<const uint32_t*>(&y);
           }
         }
-        if constexpr (kExact) {
-          float a[8];
-          uint32_t vl[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t ch = pair_s[(wk >> (8 * x)) & 255u][copy], cl = res_s[(wk >> (8 * x)) & 255u][copy];
-            const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&ch)), lf = __half22float2(*reinterpret_cast<const __half2*>(&cl));
-            const float n = fits ? kn : __uint_as_float(0x7FC00000u);
-            a[2 * x] = (hf.x + lf.x) * n;
-            a[2 * x + 1] = (hf.y + lf.y) * n;
-            vl[x] = res_s[(wv >> (8 * x)) & 255u][copy];
-          }
-          rg_store_row<true>(k0 + i * kD, kv_part, a);
-          *reinterpret_cast<uint4*>(v0 + kv_part + i * kD + lane * 8) = make_uint4(vl[0], vl[1], vl[2], vl[3]);
-        } else {
-          *reinterpret_cast<uint4*>(k0 + i * kD + lane * 8) = make_uint4(kk[0], kk[1], kk[2], kk[3]);
-        }
+        *reinterpret_cast<uint4*>(k0 + i * kD + lane * 8) = make_uint4(kk[0], kk[1], kk[2], kk[3]);
         *reinterpret_cast<uint4*>(v0 + i * kD + lane * 8) = make_uint4(vv[0], vv[1], vv[2], vv[3]);
-        mine = fits ? vn * Sh::kPScale : 0.f;
+        if constexpr (kExact) {
+          *reinterpret_cast<uint4*>(k0 + kv_part + i * kD + lane * 8) = make_uint4(kl[0], kl[1], kl[2], kl[3]);
+          *reinterpret_cast<uint4*>(v0 + kv_part + i * kD + lane * 8) = make_uint4(vl[0], vl[1], vl[2], vl[3]);
+        }
+        if (lane == 0) p.norms[int64_t(h) * p.store_rows + srow0 + i] = fits ? vn * Sh::kPScale : 0.f;
       }
-      if (lane == i) size = mine;
     }
-    if (lane < 4) p.norms[int64_t(h) * p.store_rows + srow0 + lane] = size;
-    if (bad_page && lane == 0) record_error(p.status, TQ4_ERR_PAGE_RANGE);
   }
 }
 
@@ -591,9 +690,14 @@ struct RgWalk {
   __device__ __forceinline__ RgWalk(const RaggedParams& params, int pr) : p(params), pair(pr) {
     const RgHead hd = *p.head;
     n_blk = hd.n_blk;
-    const int64_t all = p.blk_cum[n_blk] * kHkv;
-    left = int64_t(pair + 1) * all / hd.n_pairs - int64_t(pair) * all / hd.n_pairs;
+    const int64_t per_head = p.blk_cum[n_blk];
     const RgStart s = p.starts[pair];
+    int64_t end = per_head * kHkv;   // tiles before the next pair's share
+    if (pair + 1 < hd.n_pairs) {
+      const RgStart e = p.starts[pair + 1];
+      end = e.head * per_head + p.blk_cum[e.blk] + e.tile;
+    }
+    left = end - (s.head * per_head + p.blk_cum[s.blk] + s.tile);
     head = s.head;
     blk = s.blk;
     tile = s.tile;
@@ -624,28 +728,6 @@ struct RgWalk {
 // costs 900 cycles here, an acquire 400 (measured with clock64), a tile's products 2,048.
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
-}
-// two fp32 operations in one instruction
-__device__ __forceinline__ uint64_t pair_f32(float a, float b) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-  return d;
-}
-__device__ __forceinline__ void unpair_f32(uint64_t d, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d)); }
-__device__ __forceinline__ uint64_t fma2_f32(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2_f32(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2_f32(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
 }
 // 32-point Walsh-Hadamard transform in registers, element 2 i + k in half k of pair i
 __device__ __forceinline__ void fwht32(uint64_t (&v)[16]) {
@@ -1235,9 +1317,9 @@ inline cudaError_t ragged_set_attrs() {
 
 template <bool kExact>
 cudaError_t launch_ragged_t(RaggedParams& p, const CUtensorMap& qmap, const CUtensorMap& kvmap, const RgLayout& l, int num_sms, cudaStream_t st) {
-  // units of the prep: one per 32 row positions and KV head, and one per token
-  const int64_t units = l.store_rows / 32 * kHkv + p.n_tok;
-  const dim3 prep(unsigned(std::min<int64_t>(units, int64_t(num_sms) * 6) + 1));
+  // units of the prep, one a warp: four row positions of a KV head, or four of a token's queries
+  const int64_t units = l.store_rows / 4 * kHkv + int64_t(p.n_tok) * (kHq / 4);
+  const dim3 prep(unsigned(std::min<int64_t>(units, int64_t(num_sms) * 4) + 1));
   cudaError_t e = launch_pdl(ragged_prep_kernel<kExact>, prep, dim3(kRgPrepThreads), size_t(p.n_req) * 8, st, p);
   if (e != cudaSuccess) return e;
   e = launch_pdl(ragged_attend_kernel<kExact>, dim3(unsigned(2 * p.max_pairs)), dim3(kRgThreads), size_t(RgShape<kExact>::kSmem), st, p, qmap, kvmap);
