@@ -969,7 +969,7 @@ int tq4_reconstruct_slots(tq4_ctx* ctx, const void* pool, int32_t num_pages, con
 size_t tq4_decode_window_workspace_bytes(const tq4_ctx* ctx, int32_t n_req, int32_t n_q, int32_t max_pages,
                                          int32_t window, int32_t n_sink) {
   if (!ctx || n_req <= 0 || n_q < 1 || n_q > TQ4_MAX_QUERY_TOKENS || max_pages <= 0 || window < 1 || n_sink < 0) return 0;
-  return tq4::window_workspace_bytes(ctx->num_sms, n_req, n_q, max_pages, window, n_sink);
+  return tq4::window_plan(ctx->num_sms, n_req, n_q, max_pages, window, n_sink).total;
 }
 
 int tq4_decode_attention_window(tq4_ctx* ctx, const void* pool, int32_t num_pages, const uint16_t* q,
@@ -985,8 +985,8 @@ int tq4_decode_attention_window(tq4_ctx* ctx, const void* pool, int32_t num_page
   if (!aligned(pool, 16) || !aligned(q, 16) || !aligned(out, 16)) return TQ4_ERR_ARG;
   if (int64_t(max_pages) * tq4::kPage > INT32_MAX || int64_t(num_pages) * tq4::kRowsPerPage > INT32_MAX)
     return TQ4_ERR_UNSUPPORTED;
-  const size_t need = tq4::window_workspace_bytes(ctx->num_sms, n_req, n_q, max_pages, window, n_sink);
-  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return TQ4_ERR_WORKSPACE;
+  const tq4::WindowPlan pl = tq4::window_plan(ctx->num_sms, n_req, n_q, max_pages, window, n_sink);
+  if (pl.line && (!workspace || workspace_bytes < pl.total || !aligned(workspace, 256))) return TQ4_ERR_WORKSPACE;
   if (int rc = check_device(ctx)) return rc;
   CUtensorMap map;
   if (int rc = pool_tensor_map(pool, num_pages, &map)) return rc;
@@ -1002,14 +1002,24 @@ int tq4_decode_attention_window(tq4_ctx* ctx, const void* pool, int32_t num_page
   p.window = window;
   p.n_sink = n_sink;
   p.scale = scale;
-  p.splits = tq4::window_splits(ctx->num_sms, n_req, n_q, max_pages, window, n_sink);
+  p.splits = pl.splits;
+  p.num_sms = ctx->num_sms;
+  if (pl.line) {
+    char* ws = static_cast<char*>(workspace);
+    p.head = reinterpret_cast<int32_t*>(ws + pl.head);
+    p.cum_tiles = reinterpret_cast<int32_t*>(ws + pl.cum_tiles);
+    p.cum_cost = reinterpret_cast<int64_t*>(ws + pl.cum_cost);
+    p.starts = reinterpret_cast<int4*>(ws + pl.starts);
+    p.po = reinterpret_cast<float*>(ws + pl.po);
+    p.pml = reinterpret_cast<float2*>(ws + pl.pml);
+  }
   p.out = out;
   p.out_dtype = out_dtype;
   p.signs = ctx->signs;
   p.status = ctx->d_status;
   p.spin_limit = ctx->wait_polls;
   p.test_withhold = ctx->withhold;
-  return cuda_status(tq4::launch_decode_window(p, map, static_cast<cudaStream_t>(stream)));
+  return cuda_status(tq4::launch_decode_window(p, map, pl.line, static_cast<cudaStream_t>(stream)));
 }
 
 size_t tq4_prefill_ragged_workspace_bytes(const tq4_ctx* ctx, int32_t n_req, int32_t n_tok, int32_t max_pages,

@@ -8,13 +8,16 @@
 //   s_j = n_j (R q) . c[idx_j] * scale,  o = R^T sum_j p_j n_j c[idx_j] / sum_j p_j.
 //
 // Work split. Only the 32-position tiles that some query token sees are visited: those
-// of the sinks, then those of the window. A cluster of CS CTAs owns one (request, KV
-// head); its 8 CS warps take the visible tiles in turn, each through its own two-stage
-// TMA ring, and the partial results meet in shared memory, first in the CTA, then over
-// the cluster's distributed shared memory, where each output row is merged, rotated
-// back and stored by one warp. So the call is one launch and needs no workspace: a
-// window bounds the work per request, and the second launch of a split-K scheme
-// (~3.5 us) would cost as much as the window itself.
+// of the sinks, then those of the window. The warps of a CTA take them in turn, each
+// through its own two-stage TMA ring, and their results meet in shared memory.
+//   clusters (few requests): a cluster of up to 8 CTAs owns one (request, KV head); its
+//     partial results meet over distributed shared memory, where each output row is
+//     merged, rotated back and stored by one warp. One launch, no workspace.
+//   the line (kLine, many requests): all tiles of all (KV head, request) items stand in
+//     one line, of which each of one CTA per SM takes an equal part by cost (tiles, and
+//     an item's own overhead); a plan kernel lays out the parts from the lengths, and a
+//     combine kernel merges items that several CTAs share. Lengths of any mixture keep
+//     every SM busy to the end, for two more launches.
 //
 // One token (NT = 1 n-tile: 6 query heads padded to 8): a warp keeps all 256 dims of
 // its rows' sums in registers. 2-4 tokens (NT = 2, 3): those would be 128-192 registers,
@@ -45,6 +48,14 @@ struct WindowParams {
   int32_t n_sink;
   float scale;
   int32_t splits;        // CTAs per (request, KV head) = cluster size
+  int32_t num_sms;
+  // the line's workspace
+  int32_t* head;         // [0] CTAs with work
+  int32_t* cum_tiles;    // [n_req + 1] tiles before each request, one KV head
+  int64_t* cum_cost;     // [n_req + 1] likewise their cost
+  int4* starts;          // [num_sms] {KV head, request, first tile, tiles} of each CTA's part
+  float* po;             // [2 num_sms][24 rows][256] results of items' parts, and their (m, l)
+  float2* pml;           // [2 num_sms][24]
   void* out;
   int out_dtype;
   Signs signs;
@@ -126,7 +137,20 @@ __device__ __forceinline__ void wd_store_row(const WindowParams& p, int64_t row,
   }
 }
 
-template <int NT, bool kExact>
+// The tiles that a request's query tokens see: those of sinks [0, sinks), then, `skip` further on, all from the
+// first window's first to the last position's. n = 0: padding or a bad length.
+struct WdSpan { int32_t sinks, skip, n; };
+__device__ __forceinline__ WdSpan wd_span(const WindowParams& p, int32_t T) {
+  WdSpan s{0, 0, 0};
+  if (T < p.n_q || int64_t(T) > int64_t(p.max_pages) * kPage) return s;
+  const int lo = max(0, T - p.n_q - p.window + 1);            // first position inside a window
+  s.sinks = (min(p.n_sink, lo) + kQ1Tile - 1) / kQ1Tile;
+  s.skip = max(lo / kQ1Tile - s.sinks, 0);
+  s.n = (T + kQ1Tile - 1) / kQ1Tile - s.skip;
+  return s;
+}
+
+template <int NT, bool kExact, bool kLine>
 __global__ void __launch_bounds__(kQ1Threads, 1)
     decode_window_kernel(const WindowParams p, const __grid_constant__ CUtensorMap tmap) {
   constexpr bool kPair = NT > 1;
@@ -136,8 +160,7 @@ __global__ void __launch_bounds__(kQ1Threads, 1)
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int h = blockIdx.y;
-  const int r = int(blockIdx.x) / p.splits, rank = int(blockIdx.x) % p.splits;
+  const int rank = kLine ? 0 : int(blockIdx.x) % p.splits;
   // in a cluster, rank r's own shared addresses start at r << 24: the layout's fixed offsets are
   // taken from there (lut_lo and hi_buf below are shared addresses of this CTA)
   const uint32_t win = base & 0xFF000000u;
@@ -145,7 +168,7 @@ __global__ void __launch_bounds__(kQ1Threads, 1)
   const uint32_t low0 = (base + kWdCtlBytes + 1023) & ~1023u;
   if (low0 + kWdLowBufs * kQ1Buf > lut_lo) {   // the layout needs the dynamic window to start low
     if (tid == 0) record_error(p.status, TQ4_ERR_CUDA);
-    if (p.splits > 1) {   // the others of the cluster may be at work: keep their barriers and this memory alive
+    if (!kLine && p.splits > 1) {   // the others of the cluster may be at work: keep their barriers and this memory alive
       wd_cluster_sync();
       wd_cluster_sync();
     }
@@ -174,43 +197,78 @@ __global__ void __launch_bounds__(kQ1Threads, 1)
   pdl_launch_dependents();
 
   const int n_rows = kGroup * p.n_q;
-  const int T = __ldg(p.seq_lens + r);
   const uint32_t sb = lane_sign_bits(p.signs);
-  const int64_t out_row0 = int64_t(r) * p.n_q * kHq + h * kGroup;   // + token * 24 + head
-  if (T < p.n_q || int64_t(T) > int64_t(p.max_pages) * kPage) {   // a padded request (0), or a bad length
-    if (rank == 0) {
-      if (T != 0 && tid == 0) record_error(p.status, TQ4_ERR_SEQ);
-      for (int row = w; row < n_rows; row += kQ1Warps) {
-        float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        wd_store_row(p, out_row0 + (row / kGroup) * kHq + row % kGroup, z, 0.f, 0u);
-      }
+  auto zero_rows = [&](int r, int h) {   // of a padded request, or one of a bad length
+    const int64_t row0 = int64_t(r) * p.n_q * kHq + h * kGroup;
+    for (int row = w; row < n_rows; row += kQ1Warps) {
+      float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      wd_store_row(p, row0 + (row / kGroup) * kHq + row % kGroup, z, 0.f, 0u);
     }
-    return;   // the same in every CTA of the cluster
+  };
+  bool timed_out = false;
+  // line: this CTA's stretches in order. Clusters: one, tiles dealt out over the cluster's CTAs.
+  int h = kLine ? 0 : int(blockIdx.y), r = kLine ? 0 : int(blockIdx.x) / p.splits;
+  int a0 = 0, left = 0, done_own = 0, done_other = 0;   // first tile; tiles to do; tiles that this warp's (its partner's) ring has seen
+  bool first_stretch = true;
+  if constexpr (kLine) {
+    for (int x = blockIdx.x; x < p.n_req; x += gridDim.x) {
+      const int T = __ldg(p.seq_lens + x);
+      if (wd_span(p, T).n > 0) continue;
+      if (T != 0 && tid == 0) record_error(p.status, TQ4_ERR_SEQ);
+      for (int y = 0; y < kHkv; ++y) zero_rows(x, y);
+    }
+    if (int(blockIdx.x) >= p.head[0]) return;
+    const int4 st = p.starts[blockIdx.x];
+    h = st.x;
+    r = st.y;
+    a0 = st.z;
+    left = st.w;
+  }
+#pragma unroll 1
+  do {
+  if (kLine && h >= kHkv) break;   // (lengths that changed since the plan)
+  const int T = __ldg(p.seq_lens + r);
+  const int64_t out_row0 = int64_t(r) * p.n_q * kHq + h * kGroup;   // + token * 24 + head
+  const WdSpan span = wd_span(p, T);
+  if constexpr (!kLine) {
+    if (span.n == 0) {
+      if (rank == 0) {
+        if (T != 0 && tid == 0) record_error(p.status, TQ4_ERR_SEQ);
+        zero_rows(r, h);
+      }
+      return;   // the same in every CTA of the cluster
+    }
+  } else if (span.n == 0) {   // passed over (its rows are zero already)
+    ++r;
+    if (r == p.n_req) {
+      r = 0;
+      ++h;
+    }
+    continue;
   }
   const int first = T - p.n_q;                                // position of query token 0
-  const int lo = max(0, first - p.window + 1);                // first position inside a window
-  const int a_t = (min(p.n_sink, lo) + kQ1Tile - 1) / kQ1Tile;   // sink tiles
-  const int skip = max(lo / kQ1Tile - a_t, 0);                // tiles between the sinks and the window
-  const int n_tiles = (T + kQ1Tile - 1) / kQ1Tile - skip;
+  const int a_t = span.sinks, skip = span.skip;
+  const int end = kLine ? min(span.n, a0 + left) : span.n;    // tiles [a0, end) of the item
+  const bool whole = !kLine || (a0 == 0 && end == span.n);
   const int32_t* const table = p.tables + int64_t(r) * p.max_pages;
   // visible tile i (in order) -> its first position; tile k of this warp
+  const int per = (kLine ? 1 : p.splits) * kQ1Warps, at_w = a0 + rank * kQ1Warps;
   auto tile_pos = [&](int k) {
-    const int i = (k * p.splits + rank) * kQ1Warps + w;
+    const int i = at_w + k * per + w;
     return (i < a_t ? i : i + skip) * kQ1Tile;
   };
-  auto tile_ok = [&](int k) { return (k * p.splits + rank) * kQ1Warps + w < n_tiles; };
+  auto tile_ok = [&](int k) { return at_w + k * per + w < end; };
   const int lead = kPair ? w & ~1 : w;                        // both warps of a pair make the same rounds
-  const int per = p.splits * kQ1Warps, at0 = rank * kQ1Warps + lead;
-  const int rounds = n_tiles > at0 ? (n_tiles - at0 + per - 1) / per : 0;
+  const int rounds = end > at_w + lead ? (end - at_w - lead + per - 1) / per : 0;
+  auto ring = [&](int k) { return done_own + k; };            // this warp's count of tile k
   auto tile_page = [&](int k) -> int32_t { return k < rounds && tile_ok(k) ? __ldg(table + (tile_pos(k) >> 8)) : -1; };
-  bool timed_out = false;
   int issued = 0;   // tiles whose copies this warp has started (its first `issued` rounds)
   auto issue_tile = [&](int k, int32_t page) {
     if (k >= rounds || timed_out) return;
     issued = k + 1;
     if (lane == 0 && tile_ok(k) && !(p.test_withhold && k == 0)) {
       const int c = tile_pos(k);
-      const int b = w * kQ1Stages + (k % kQ1Stages);
+      const int b = w * kQ1Stages + (ring(k) % kQ1Stages);
       const uint32_t bar = base + kWdBarOff + b * 8;
       if (page < 0 || page >= p.num_pages) {
         record_error(p.status, TQ4_ERR_PAGE_RANGE);
@@ -318,20 +376,20 @@ __global__ void __launch_bounds__(kQ1Threads, 1)
       issue_tile(k + 1, page_next);
       page_next = tile_page(k + 2);
     }
-    const int b = w * kQ1Stages + (k % kQ1Stages);
+    const int b = w * kQ1Stages + (ring(k) % kQ1Stages);
     bool have = tile_ok(k);
-    auto wait_tile = [&](int buf) {
+    auto wait_tile = [&](int buf, int count) {
       const uint32_t bar = base + kWdBarOff + buf * 8;
       uint32_t spins = 0;
       bool late = timed_out;
-      while (!late && !mbar_try_wait(bar, (k / kQ1Stages) & 1)) late = ++spins > p.spin_limit;
+      while (!late && !mbar_try_wait(bar, (count / kQ1Stages) & 1)) late = ++spins > p.spin_limit;
       if (__any_sync(0xffffffffu, late)) {
         if (lane == 0 && !timed_out) record_error(p.status, TQ4_ERR_TIMEOUT);
         timed_out = true;
       }
       return !timed_out;
     };
-    if (have) have = wait_tile(b);   // warp-uniform; a pair keeps its rounds either way
+    if (have) have = wait_tile(b, ring(k));   // warp-uniform; a pair keeps its rounds either way
     if (!kPair && !have) break;
     const uint32_t kst = buf_addr(b);
     const uint32_t nb = base + kWdNrmOff + b * 128;
@@ -584,8 +642,8 @@ __global__ void __launch_bounds__(kQ1Threads, 1)
       // order these stores before the copy that refills the buffer two rounds on
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       pair_sync(w >> 1);
-      const int bp = (w ^ 1) * kQ1Stages + (k % kQ1Stages);
-      const bool have_p = (k * p.splits + rank) * kQ1Warps + (w ^ 1) < n_tiles && wait_tile(bp);
+      const int bp = (w ^ 1) * kQ1Stages + ((done_other + k) % kQ1Stages);
+      const bool have_p = at_w + k * per + (w ^ 1) < end && wait_tile(bp, done_other + k);
       if (have) v_phase(kst + kQ1KV, bh, bl);
       if (have_p) {
         const uint32_t pst = buf_addr(bp);
@@ -609,9 +667,9 @@ __global__ void __launch_bounds__(kQ1Threads, 1)
   if (timed_out) {
     for (int k = max(issued - kQ1Stages, 0); k < issued; ++k) {
       if (!tile_ok(k) || (p.test_withhold && k == 0)) continue;
-      const uint32_t bar = base + kWdBarOff + (w * kQ1Stages + (k % kQ1Stages)) * 8;
+      const uint32_t bar = base + kWdBarOff + (w * kQ1Stages + (ring(k) % kQ1Stages)) * 8;
       uint32_t spins = 0;
-      while (!mbar_try_wait(bar, (k / kQ1Stages) & 1) && ++spins < kQ1DrainPolls) {
+      while (!mbar_try_wait(bar, (ring(k) / kQ1Stages) & 1) && ++spins < kQ1DrainPolls) {
       }
     }
   }
@@ -693,7 +751,15 @@ __global__ void __launch_bounds__(kQ1Threads, 1)
       acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
       acc[4] += bb.x; acc[5] += bb.y; acc[6] += bb.z; acc[7] += bb.w;
     }
-    if (p.splits == 1) {
+    if (kLine && !whole) {   // this stretch's part of the row, for the combine
+      if (row < n_rows) {
+        const int64_t rec = int64_t(2 * int(blockIdx.x) + (first_stretch ? 0 : 1)) * 24 + row;
+        float4* dst = reinterpret_cast<float4*>(p.po + rec * kD + lane * 8);
+        dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (lane == 0) p.pml[rec] = make_float2(M, L);
+      }
+    } else if (kLine || p.splits == 1) {
       if (row < n_rows)
         wd_store_row(p, out_row0 + (row / kGroup) * kHq + row % kGroup, acc,
                      L > 0.f ? 0.0625f / (wd_pscale<kExact>() * L) : 0.f, sb);
@@ -703,6 +769,22 @@ __global__ void __launch_bounds__(kQ1Threads, 1)
     }
     row_m[n] = M;
     row_l[n] = L;
+  }
+  if constexpr (kLine) {
+    // the next stretch: the ring goes on, and its copies may replace what was merged here
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+    __syncthreads();
+    const int n = end - a0, other = w ^ 1;
+    done_own += n > w ? (n - w + kQ1Warps - 1) / kQ1Warps : 0;
+    done_other += n > other ? (n - other + kQ1Warps - 1) / kQ1Warps : 0;
+    left -= n;
+    first_stretch = false;
+    a0 = 0;
+    if (++r == p.n_req) {
+      r = 0;
+      ++h;
+    }
+    continue;
   }
   if (p.splits == 1) return;
   __syncthreads();   // every warp has read m and l of all warps
@@ -739,6 +821,116 @@ __global__ void __launch_bounds__(kQ1Threads, 1)
     wd_store_row(p, out_row0 + (row / kGroup) * kHq + row % kGroup, acc, L > 0.f ? 0.0625f / (wd_pscale<kExact>() * L) : 0.f, sb);
   }
   wd_cluster_sync();   // no CTA leaves while another reads its shared memory
+  } while (kLine && left > 0);
+}
+
+// --------------------------------------------------------------------------
+// The line's plan, one CTA: tiles and cost of the requests, their running sums, and the parts. A cut inside an
+// item's overhead lies before its first tile; parts of at least the overhead and a round of tiles are never empty.
+// --------------------------------------------------------------------------
+constexpr int kWdItemCost = 16;   // an item's queries and merge against a tile's time (bf16, one token: 4 us and 0.25 us)
+constexpr int kWdPlanThreads = 1024;
+__global__ void __launch_bounds__(kWdPlanThreads) decode_window_plan_kernel(const WindowParams p) {
+  __shared__ int64_t tot[2][32], carry[2];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  if (tid < 2) carry[tid] = 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  __syncthreads();
+  for (int base = 0; base < p.n_req; base += kWdPlanThreads) {
+    const int r = base + tid;
+    const int64_t n = r < p.n_req ? wd_span(p, p.seq_lens[r]).n : 0, c = n > 0 ? n + kWdItemCost : 0;
+    int64_t sn = n, sc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t un = __shfl_up_sync(0xffffffffu, sn, o), uc = __shfl_up_sync(0xffffffffu, sc, o);
+      if (lane >= o) {
+        sn += un;
+        sc += uc;
+      }
+    }
+    if (lane == 31) {
+      tot[0][w] = sn;
+      tot[1][w] = sc;
+    }
+    __syncthreads();
+    int64_t bn = carry[0] + sn - n, bc = carry[1] + sc - c;
+    for (int x = 0; x < w; ++x) {
+      bn += tot[0][x];
+      bc += tot[1][x];
+    }
+    if (r < p.n_req) {
+      p.cum_tiles[r] = int32_t(bn);
+      p.cum_cost[r] = bc;
+    }
+    __syncthreads();
+    if (tid < 2)
+      for (int x = 0; x < kWdPlanThreads / 32; ++x) carry[tid] += tot[tid][x];
+    __syncthreads();
+  }
+  const int64_t tiles_head = carry[0], cost_head = carry[1], cost = cost_head * kHkv;
+  const int n_cta = int(min(int64_t(p.num_sms), cost > 0 ? max(cost / (kWdItemCost + kQ1Warps), int64_t(1)) : int64_t(0)));
+  if (tid == 0) p.head[0] = n_cta;
+  // where part x begins, and the tiles before it
+  auto start = [&](int x, int4& at) -> int64_t {
+    if (x == n_cta) return tiles_head * kHkv;
+    const int64_t g = int64_t(x) * cost / n_cta, head = g / cost_head, in = g - head * cost_head;
+    int lo = 0, hi = p.n_req - 1;   // the last request whose cost begins at or before it (requests without tiles have none)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.cum_cost[mid] <= in) lo = mid;
+      else hi = mid - 1;
+    }
+    const int tile = int(max(in - p.cum_cost[lo] - kWdItemCost, int64_t(0)));
+    at = make_int4(int(head), lo, tile, 0);
+    return head * tiles_head + p.cum_tiles[lo] + tile;
+  };
+  for (int x = tid; x < n_cta; x += kWdPlanThreads) {
+    int4 at, next;
+    const int64_t begin = start(x, at);
+    at.w = int(start(x + 1, next) - begin);
+    p.starts[x] = at;
+  }
+}
+
+// The line's combine: CTA (b, row) looks at the border before part b + 1; where it is the first one inside an item,
+// that item's row is merged from its parts, o = R^T sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
+template <bool kExact>
+__global__ void __launch_bounds__(32 * kQ1Warps) decode_window_combine_kernel(const WindowParams p) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, b = int(blockIdx.x) + 1;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int n_cta = p.head[0];
+  if (b >= n_cta) return;
+  const int4 me = p.starts[b], prev = p.starts[b - 1];
+  if (me.z == 0) return;                                               // no item is cut here
+  const bool same = prev.x == me.x && prev.y == me.y;
+  if (same && prev.z > 0) return;                                      // not its first cut
+  const int part0 = 2 * (b - 1) + (same ? 0 : 1);
+  auto more = [&](int i) {   // part i begins inside the item
+    if (i >= n_cta) return false;
+    const int4 s = p.starts[i];
+    return s.x == me.x && s.y == me.y;
+  };
+  const uint32_t sb = lane_sign_bits(p.signs);
+  const int64_t out_row0 = int64_t(me.y) * p.n_q * kHq + me.x * kGroup;
+  for (int row = w; row < kGroup * p.n_q; row += kQ1Warps) {
+    float M = p.pml[int64_t(part0) * 24 + row].x;
+    for (int i = b; more(i); ++i) M = fmaxf(M, p.pml[int64_t(2 * i) * 24 + row].x);
+    float L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int i = b - 1; i < b || more(i); ++i) {
+      const int64_t rec = int64_t(i < b ? part0 : 2 * i) * 24 + row;
+      const float2 ml = p.pml[rec];
+      if (ml.x == -INFINITY && ml.y == 0.f) continue;   // that part showed this row nothing
+      const float f = fast_exp2(ml.x - M);
+      L = fmaf(f, ml.y, L);
+      const float4* src = reinterpret_cast<const float4*>(p.po + rec * kD + lane * 8);
+      const float4 x = src[0], y = src[1];
+      acc[0] = fmaf(f, x.x, acc[0]); acc[1] = fmaf(f, x.y, acc[1]); acc[2] = fmaf(f, x.z, acc[2]); acc[3] = fmaf(f, x.w, acc[3]);
+      acc[4] = fmaf(f, y.x, acc[4]); acc[5] = fmaf(f, y.y, acc[5]); acc[6] = fmaf(f, y.z, acc[6]); acc[7] = fmaf(f, y.w, acc[7]);
+    }
+    wd_store_row(p, out_row0 + (row / kGroup) * kHq + row % kGroup, acc, L == 0.f ? 0.f : 0.0625f / (wd_pscale<kExact>() * L), sb);
+  }
 }
 
 inline cudaError_t window_set_attrs() {
@@ -746,28 +938,63 @@ inline cudaError_t window_set_attrs() {
   auto set = [&e](const void* k) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kWdDynBytes));
   };
-  set(reinterpret_cast<const void*>(decode_window_kernel<1, false>));
-  set(reinterpret_cast<const void*>(decode_window_kernel<1, true>));
-  set(reinterpret_cast<const void*>(decode_window_kernel<2, false>));
-  set(reinterpret_cast<const void*>(decode_window_kernel<2, true>));
-  set(reinterpret_cast<const void*>(decode_window_kernel<3, false>));
-  set(reinterpret_cast<const void*>(decode_window_kernel<3, true>));
+#define WD_SET(NT)                                                                     \
+  set(reinterpret_cast<const void*>(decode_window_kernel<NT, false, false>));           \
+  set(reinterpret_cast<const void*>(decode_window_kernel<NT, true, false>));            \
+  set(reinterpret_cast<const void*>(decode_window_kernel<NT, false, true>));            \
+  set(reinterpret_cast<const void*>(decode_window_kernel<NT, true, true>))
+  WD_SET(1);
+  WD_SET(2);
+  WD_SET(3);
+#undef WD_SET
   return e;
 }
 
-// CTAs per (request, KV head): the largest power of two up to kWdMaxCluster that keeps the
-// launch within one CTA per SM, but no more than there are rounds of 8 tiles to share out.
-inline int window_splits(int num_sms, int32_t n_req, int32_t n_q, int32_t max_pages, int32_t window, int32_t n_sink) {
+// How a call is split, and its workspace. Tiles a request can have at most:
+struct WindowPlan {
+  bool line;
+  int splits;   // CTAs per (request, KV head) without the line: the largest power of two up to
+                // kWdMaxCluster that keeps the launch within one CTA per SM, but no more than there are
+                // rounds of 8 tiles to share out
+  size_t head, cum_tiles, cum_cost, starts, po, pml, total;
+};
+// What the line's two more launches cost in tiles' time: 6 us at 0.25 us a tile (one token), 1 us (several).
+constexpr int64_t kWdLineFrom1 = 24, kWdLineFrom = 6;
+inline WindowPlan window_plan(int num_sms, int32_t n_req, int32_t n_q, int32_t max_pages, int32_t window, int32_t n_sink) {
+  WindowPlan pl{};
   const int64_t most = std::min<int64_t>(int64_t(max_pages) * kPage, int64_t(window) + n_q - 1 + n_sink + 3 * kQ1Tile);
-  const int64_t tiles = (most + kQ1Tile - 1) / kQ1Tile;
-  int s = 1;
-  while (s < kWdMaxCluster && int64_t(n_req) * kHkv * s * 2 <= num_sms && tiles > s * kQ1Warps) s *= 2;
-  return s;
+  const int64_t tiles = (most + kQ1Tile - 1) / kQ1Tile, units = int64_t(n_req) * kHkv;
+  pl.splits = 1;
+  while (pl.splits < kWdMaxCluster && units * pl.splits * 2 <= num_sms && tiles > pl.splits * kQ1Warps) pl.splits *= 2;
+  // the longest CTA's tiles with clusters against the mean with the line
+  const int64_t waves = (units * pl.splits + num_sms - 1) / num_sms;
+  pl.line = waves * ((tiles + pl.splits - 1) / pl.splits) > units * tiles / num_sms + (decode_nt(n_q) == 1 ? kWdLineFrom1 : kWdLineFrom);
+  if (!pl.line) return pl;
+  size_t at = 0;
+  auto take = [&at](size_t bytes) {
+    const size_t x = at;
+    at += (bytes + 255) & ~size_t(255);
+    return x;
+  };
+  pl.head = take(16);
+  pl.cum_tiles = take((size_t(n_req) + 1) * 4);
+  pl.cum_cost = take((size_t(n_req) + 1) * 8);
+  pl.starts = take(size_t(num_sms) * sizeof(int4));
+  pl.po = take(size_t(2 * num_sms) * 24 * kD * 4);
+  pl.pml = take(size_t(2 * num_sms) * 24 * 8);
+  pl.total = at;
+  return pl;
 }
 
-inline size_t window_workspace_bytes(int, int32_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
-
-inline cudaError_t launch_decode_window(const WindowParams& p, const CUtensorMap& map, cudaStream_t stream) {
+template <int NT, bool kExact>
+cudaError_t launch_decode_window_t(const WindowParams& p, const CUtensorMap& map, bool line, cudaStream_t stream) {
+  if (line) {
+    cudaError_t e = launch_pdl(decode_window_plan_kernel, dim3(1), dim3(kWdPlanThreads), 0, stream, p);
+    if (e == cudaSuccess)
+      e = launch_pdl(decode_window_kernel<NT, kExact, true>, dim3(unsigned(p.num_sms)), dim3(kQ1Threads), size_t(kWdDynBytes), stream, p, map);
+    if (e != cudaSuccess || p.num_sms < 2) return e;
+    return launch_pdl(decode_window_combine_kernel<kExact>, dim3(unsigned(p.num_sms - 1)), dim3(32 * kQ1Warps), 0, stream, p);
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(p.n_req) * unsigned(p.splits), kHkv);
   cfg.blockDim = dim3(kQ1Threads);
@@ -782,11 +1009,14 @@ inline cudaError_t launch_decode_window(const WindowParams& p, const CUtensorMap
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, decode_window_kernel<NT, kExact, false>, p, map);
+}
+inline cudaError_t launch_decode_window(const WindowParams& p, const CUtensorMap& map, bool line, cudaStream_t stream) {
   const bool exact = p.out_dtype == TQ4_DTYPE_F32;
   switch (decode_nt(p.n_q)) {
-    case 1: return exact ? cudaLaunchKernelEx(&cfg, decode_window_kernel<1, true>, p, map) : cudaLaunchKernelEx(&cfg, decode_window_kernel<1, false>, p, map);
-    case 2: return exact ? cudaLaunchKernelEx(&cfg, decode_window_kernel<2, true>, p, map) : cudaLaunchKernelEx(&cfg, decode_window_kernel<2, false>, p, map);
-    default: return exact ? cudaLaunchKernelEx(&cfg, decode_window_kernel<3, true>, p, map) : cudaLaunchKernelEx(&cfg, decode_window_kernel<3, false>, p, map);
+    case 1: return exact ? launch_decode_window_t<1, true>(p, map, line, stream) : launch_decode_window_t<1, false>(p, map, line, stream);
+    case 2: return exact ? launch_decode_window_t<2, true>(p, map, line, stream) : launch_decode_window_t<2, false>(p, map, line, stream);
+    default: return exact ? launch_decode_window_t<3, true>(p, map, line, stream) : launch_decode_window_t<3, false>(p, map, line, stream);
   }
 }
 

@@ -988,8 +988,8 @@ class Context:
         n = slots.numel()
         num_pages = _pool_pages(pool, self.device)
         _need("slots", slots, torch.int64, (n,), self.device)
-        kv = torch.empty((2, n, KV_HEADS, HEAD_DIM), dtype=out_dtype, device=self.device)
-        k, v = kv.unbind(0)
+        k = torch.empty((n, KV_HEADS, HEAD_DIM), dtype=out_dtype, device=self.device)
+        v = torch.empty_like(k)
         _check(_lib.tq4_reconstruct_slots(self.handle, pool.data_ptr(), num_pages, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
                                           code, self._stream(stream)), "tq4_reconstruct_slots")
         return k, v

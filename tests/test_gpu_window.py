@@ -130,6 +130,37 @@ def test_cluster_sizes(ctx, dtype, n_req, n_q):
     _run(ctx, lens, n_q, 3000, 70, dtype, seed=n_req)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n_q,window,sinks", [(1, 2500, 40), (1, BIG, 0), (2, 2500, 0), (3, BIG, 5), (4, 2000, 300)])
+def test_a_line_of_ragged_requests(ctx, dtype, n_q, window, sinks):
+    """Sixty requests, padding among them: the tiles of all stand in one line, cut into equal parts."""
+    rng = np.random.default_rng(60 + n_q)
+    lens = [int(x) for x in rng.integers(n_q, 900, 60)]
+    lens[::9] = [0] * len(lens[::9])
+    lens[3], lens[11], lens[30], lens[59] = 3000, n_q, 2817, 2500
+    ws = ctx.decode_window_workspace(60, n_q, 12, window, sinks)
+    assert ws.numel() > 256   # the line's workspace
+    _run(ctx, lens, n_q, window, sinks, dtype, seed=7)
+    _run(ctx, [0] * 59 + [1500], n_q, window, sinks, dtype, seed=8)
+
+
+def test_a_line_without_work(ctx):
+    rng = np.random.default_rng(1)
+    pool = torch.from_numpy(random_pool(rng, 2)).cuda()
+    out = torch.ones((80, 2, 24, 256), dtype=torch.bfloat16, device="cuda")
+    tab = torch.full((80, 30), -1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(80, dtype=torch.int32, device="cuda")
+    args = (pool, torch.ones_like(out), tab, lens, BIG, 0, SCALE)
+    ctx.decode_attention_window(*args, out=out)
+    assert ctx.status() == tq4.TQ4_OK and not out.any()
+    lens[5] = 1   # below the two tokens
+    ctx.decode_attention_window(*args, out=out.fill_(1))
+    assert ctx.status() == tq4.TQ4_ERR_SEQ and not out.any()
+    with pytest.raises(tq4.TQ4Error) as e:
+        ctx.decode_attention_window(*args, out=out, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == tq4.TQ4_ERR_WORKSPACE
+
+
 def test_other_scales(ctx):
     for scale in (1.0, -0.05, 0.0, 1e-3):
         _run(ctx, [700, 90], 2, 500, 3, torch.float32, scale=scale)
@@ -217,13 +248,14 @@ def test_repeats_bit_for_bit_on_two_streams(ctx):
 
 def test_wait_that_runs_out_is_reported_and_the_context_recovers(ctx):
     args = ([1200, 400], 1, 600, 4, torch.float32)
-    for n_q in (1, 3):
+    for n_q, n_req in ((1, 1), (3, 1), (1, 40), (4, 40)):
         rng = np.random.default_rng(0)
-        tab, pages = scattered(rng, [1200])
+        tab, pages = scattered(rng, [3000])
         pool = torch.from_numpy(random_pool(rng, pages)).cuda()
-        q = torch.ones((1, n_q, 24, 256), dtype=torch.bfloat16, device="cuda")
+        q = torch.ones((n_req, n_q, 24, 256), dtype=torch.bfloat16, device="cuda")
         ctx.set_wait_limit(2000, withhold_signal=True)
-        ctx.decode_attention_window(pool, q, torch.from_numpy(tab).cuda(), torch.tensor([1200], dtype=torch.int32, device="cuda"), 600, 4, SCALE)
+        ctx.decode_attention_window(pool, q, torch.from_numpy(tab).cuda().expand(n_req, -1).contiguous(),
+                                    torch.full((n_req,), 3000, dtype=torch.int32, device="cuda"), 2800, 4, SCALE)
         torch.cuda.synchronize()
         ctx.set_wait_limit(0)
         assert ctx.status() == tq4.TQ4_ERR_TIMEOUT
