@@ -832,6 +832,11 @@ constexpr int kWdItemCost = 16;   // an item's queries and merge against a tile'
 constexpr int kWdPlanThreads = 1024;
 __global__ void __launch_bounds__(kWdPlanThreads) decode_window_plan_kernel(const WindowParams p) {
   __shared__ int64_t tot[2][32], carry[2];
+  __shared__ int64_t cost_s[kWdPlanThreads];   // the sums of a batch of one round, near at hand for the bisections
+  __shared__ int32_t tiles_s[kWdPlanThreads];
+  const bool small = p.n_req <= kWdPlanThreads;
+  int64_t* const cum_cost = small ? cost_s : p.cum_cost;
+  int32_t* const cum_tiles = small ? tiles_s : p.cum_tiles;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   if (tid < 2) carry[tid] = 0;
   pdl_wait();
@@ -860,8 +865,8 @@ __global__ void __launch_bounds__(kWdPlanThreads) decode_window_plan_kernel(cons
       bc += tot[1][x];
     }
     if (r < p.n_req) {
-      p.cum_tiles[r] = int32_t(bn);
-      p.cum_cost[r] = bc;
+      cum_tiles[r] = int32_t(bn);
+      cum_cost[r] = bc;
     }
     __syncthreads();
     if (tid < 2)
@@ -878,12 +883,12 @@ __global__ void __launch_bounds__(kWdPlanThreads) decode_window_plan_kernel(cons
     int lo = 0, hi = p.n_req - 1;   // the last request whose cost begins at or before it (requests without tiles have none)
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (p.cum_cost[mid] <= in) lo = mid;
+      if (cum_cost[mid] <= in) lo = mid;
       else hi = mid - 1;
     }
-    const int tile = int(max(in - p.cum_cost[lo] - kWdItemCost, int64_t(0)));
+    const int tile = int(max(in - cum_cost[lo] - kWdItemCost, int64_t(0)));
     at = make_int4(int(head), lo, tile, 0);
-    return head * tiles_head + p.cum_tiles[lo] + tile;
+    return head * tiles_head + cum_tiles[lo] + tile;
   };
   for (int x = tid; x < n_cta; x += kWdPlanThreads) {
     int4 at, next;

@@ -334,7 +334,7 @@ __device__ __forceinline__ void rg_store4(__half* row, int64_t part_stride, cons
 constexpr uint32_t kRgTop = 0x48FFFFFFu;
 
 template <bool kExact>
-__global__ void __launch_bounds__(kRgPrepThreads) ragged_prep_kernel(const RaggedParams p) {
+__global__ void __launch_bounds__(kRgPrepThreads, 2) ragged_prep_kernel(const __grid_constant__ RaggedParams p) {
   using Sh = RgShape<kExact>;
   constexpr int kTile = Sh::kTile;
   extern __shared__ int32_t prep_smem[];
@@ -543,30 +543,27 @@ __global__ void __launch_bounds__(kRgPrepThreads) ragged_prep_kernel(const Ragge
       const int32_t pos = pos0 + sub;
       const bool mine = pos >= first && pos < T;
       const int64_t off = (int64_t(row0 + pos - first) * kHkv + h) * kD + at8;
-      uint4 raw_v[4];
+      uint4 raw_k[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        raw[c] = mine ? __ldg(reinterpret_cast<const uint4*>(p.k + off + 64 * c)) : make_uint4(0, 0, 0, 0);
-        raw_v[c] = mine ? __ldg(reinterpret_cast<const uint4*>(p.v + off + 64 * c)) : make_uint4(0, 0, 0, 0);
+        raw[c] = mine ? __ldg(reinterpret_cast<const uint4*>(p.v + off + 64 * c)) : make_uint4(0, 0, 0, 0);
+        raw_k[c] = mine ? __ldg(reinterpret_cast<const uint4*>(p.k + off + 64 * c)) : make_uint4(0, 0, 0, 0);
       }
-      RgVec vv;
-      const uint32_t ktop = rg_rotate4(raw, mask, vec), vtop = rg_rotate4(raw_v, mask, vv);
-      const bool fits = ktop <= kRgTop && vtop <= kRgTop;
+      const uint32_t vtop = rg_rotate4(raw, mask, vec);
+      const bool v_fits = vtop <= kRgTop;
       const int e = rg_exponent(vtop);
-      if (mine) {
-        if (!fits) {   // zeros and a NaN key
+      if (!v_fits) {   // zeros here and a NaN key
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              vec.v[c][x] = 0x7FC000007FC00000ull;
-              vv.v[c][x] = 0ull;
-            }
-        }
-        rg_store4<kExact>(k0 + sub * kD, kv_part, vec, 0.0625f);
-        rg_store4<kExact>(v0 + sub * kD, kv_part, vv, rg_pow2(-e));
-        if ((lane & 7) == 0) p.norms[int64_t(h) * p.store_rows + srow0 + sub] = fits ? 0.0625f * Sh::kPScale * rg_pow2(e) : 0.f;
+          for (int x = 0; x < 4; ++x) vec.v[c][x] = 0ull;
       }
+      if (mine) {
+        rg_store4<kExact>(v0 + sub * kD, kv_part, vec, rg_pow2(-e));
+        if ((lane & 7) == 0) p.norms[int64_t(h) * p.store_rows + srow0 + sub] = v_fits ? 0.0625f * Sh::kPScale * rg_pow2(e) : 0.f;
+      }
+      const uint32_t ktop = rg_rotate4(raw_k, mask, vec);
+      if (mine) rg_store4<kExact>(k0 + sub * kD, kv_part, vec, v_fits && ktop <= kRgTop ? 0.0625f : __uint_as_float(0x7FC00000u));
     }
     if (pos0 < first || pos0 + 3 >= T) {   // cached ones, and rows that nobody sees (zeros)
       const int32_t page = pos0 < first ? __ldg(p.tables + int64_t(r) * p.max_pages + (pos0 >> 8)) : -1;   // a tile lies in one page
