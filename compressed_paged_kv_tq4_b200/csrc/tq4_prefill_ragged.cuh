@@ -1079,8 +1079,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         const RgReq rq = p.req[p.blk_req[g.blk]];
         const int rb = g.blk - rq.blk0, n_rows = min(256, 6 * rq.n_new - 256 * rb);
         const int64_t row = int64_t(g.head) * kGroup * p.n_tok + int64_t(rq.row0) * kGroup + 256 * rb;
-        // Slot s & 3 held item s - 4. Here item s - 2's last QK has run, and so item s - 4's last PV, which takes
-        // that item's P: the softmax has read its record.
+        // The copies go out first; the barrier's own arrival comes after the record, which it makes visible to all who
+        // come after the item's first product.
+        if (lane == 0) {
+          if (s > 0) ok = bounded_wait(bar(kRgQFree), (s - 1) & 1);   // the last item's last QK has run
+          if (ok) {
+#pragma unroll
+            for (int x = 0; x < Sh::kParts; ++x)
+#pragma unroll
+              for (int d = 0; d < 4; ++d)
+                tma_load_2d(sbase + x * Sh::kQPart + d * Sh::kQPanel, &qmap, 64 * d, int(x * int64_t(kHq) * p.n_tok + row + int(rank) * kPfRows),
+                            bar(kRgQFull));
+          }
+        }
+        if (!__all_sync(0xffffffffu, ok)) break;
+        // Slot s & 3 held item s - 4. Here item s - 1's last QK has run, and so item s - 3's last PV, which takes that
+        // item's P: the softmax has read its record.
         float* const fac = reinterpret_cast<float*>(smem + Sh::kFacOff) + (s & 3) * kPfRows;
 #pragma unroll
         for (int i = 0; i < kPfRows / 32; ++i) fac[32 * i + lane] = p.qfac[row + min(int(rank) * kPfRows + 32 * i + lane, n_rows - 1)];
@@ -1090,18 +1104,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
               RgItem{g.n, g.tile, span.sinks, span.skip, rq.first, 256 * rb, n_rows, g.head, rq.row0, g.part, {0, 0}};
         }
         __syncwarp();
+        ++s;
         if (lane == 0) {
-          if (s > 0) ok = bounded_wait(bar(kRgQFree), (s - 1) & 1);   // the last item's last QK has run
-          if (ok) {
-            mbar_expect_tx(bar(kRgQFull), Sh::kParts * Sh::kQPart);
-#pragma unroll
-            for (int x = 0; x < Sh::kParts; ++x)
-#pragma unroll
-              for (int d = 0; d < 4; ++d)
-                tma_load_2d(sbase + x * Sh::kQPart + d * Sh::kQPanel, &qmap, 64 * d, int(x * int64_t(kHq) * p.n_tok + row + int(rank) * kPfRows),
-                            bar(kRgQFull));
-            ++s;
-          }
+          mbar_expect_tx(bar(kRgQFull), Sh::kParts * Sh::kQPart);
           const RgSpan span = rg_block_span<kTile>(p, rq, rb);
           for (int j = 0; ok && j < g.n; ++j) {
             const int at = g.tile + j, real = at < span.sinks ? at : at + span.skip;
@@ -1123,7 +1128,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
             ++t;
           }
         }
-        s = __shfl_sync(0xffffffffu, s, 0);
         if (!__all_sync(0xffffffffu, ok)) break;
       }
       if (lane == 0 && misc[1]) {
