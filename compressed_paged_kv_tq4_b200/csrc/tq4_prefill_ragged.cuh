@@ -719,6 +719,29 @@ struct RgWalk {
   }
 };
 
+// 1 in one lane of a converged warp
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e;
+}
+// tc2_mma_ss and tc2_mma_ts of the lane whose `on` is set
+__device__ __forceinline__ void tc2_mma_ss_if(uint32_t on, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void tc2_mma_ts_if(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
 // One arrival on a barrier of the pair, at its default scope. What it orders lies in tensor memory
 // (ordered by the tcgen05 fences on both sides) or was written by a copy that has completed: no
 // generic-proxy store of this thread has to be seen by the other CTA. A release at cluster scope
@@ -1180,55 +1203,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
         }
       }
     } else {
-      // =========================================================== rank 0: MMA issuer (one thread)
-      if (lane == 0) {
-        constexpr uint32_t idesc_qk = tc_idesc(2 * kPfRows, kTile, 0);
-        constexpr uint32_t idesc_pv = tc_idesc(2 * kPfRows, kD, 1);
-        const uint64_t q0 = tc_sdesc(sbase, 16, 1024);
-        int t = 0;
-        bool ok = true;
-        while (ok && walk.next(g)) {
-          for (int j = 0; j <= g.n; ++j) {
-            if (j < g.n) {   // S[u & 1] = Q K^T
-              const int u = t + j, st = u % kStages;
-              if (!(ok = bounded_wait(bar(kRgKReady + (u & 1)), (u >> 1) & 1))) break;
-              tc_fence_after();
-              const uint32_t s_t = tmem + 128 * (u & 1);
+      // =========================================================== rank 0: MMA issuer
+      // The whole warp walks the loop and one lane's products are the ones that count: in code that only one lane
+      // runs, a product's descriptors have to be moved to uniform registers each time, and 16 products took 1,300
+      // cycles to issue instead of 1,024. (The shuffles tell the compiler what is uniform.)
+      const uint32_t leader = elect_lane();
+      constexpr uint32_t idesc_qk = tc_idesc(2 * kPfRows, kTile, 0);
+      constexpr uint32_t idesc_pv = tc_idesc(2 * kPfRows, kD, 1);
+      const uint32_t sb0 = __shfl_sync(0xffffffffu, sbase, 0), tm0 = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t q0 = tc_sdesc(sb0, 16, 1024);
+      int t = 0;
+      bool ok = true;
+      while (ok && walk.next(g)) {
+        const int n = __shfl_sync(0xffffffffu, g.n, 0);
+        for (int j = 0; j <= n; ++j) {
+          if (j < n) {   // S[u & 1] = Q K^T
+            const int u = t + j, st = u % kStages;
+            if (!(ok = warp_wait(bar(kRgKReady + (u & 1)), (u >> 1) & 1))) break;
+            tc_fence_after();
+            const uint32_t s_t = tm0 + 128 * (u & 1);
 #pragma unroll
-              for (int x = 0; x < (kExact ? 3 : 1); ++x) {   // Qh Kh, Ql Kh, Qh Kl
-                const uint64_t qx = q0 + (x == 1 ? (Sh::kQPart >> 4) : 0);
-                const uint64_t kx = tc_sdesc(sbase + Sh::kKOff + (st * Sh::kParts + (x == 2 ? 1 : 0)) * Sh::kKPart, 16, 1024);
+            for (int x = 0; x < (kExact ? 3 : 1); ++x) {   // Qh Kh, Ql Kh, Qh Kl
+              const uint64_t qx = q0 + (x == 1 ? (Sh::kQPart >> 4) : 0);
+              const uint64_t kx = tc_sdesc(sb0 + Sh::kKOff + (st * Sh::kParts + (x == 2 ? 1 : 0)) * Sh::kKPart, 16, 1024);
 #pragma unroll
-                for (int kk = 0; kk < 16; ++kk)
-                  tc2_mma_ss(s_t, qx + (((kk >> 2) * Sh::kQPanel + (kk & 3) * 32) >> 4), kx + (((kk >> 2) * Sh::kKPanel + (kk & 3) * 32) >> 4),
-                             idesc_qk, (x > 0 || kk > 0) ? 1u : 0u);
-              }
+              for (int kk = 0; kk < 16; ++kk)
+                tc2_mma_ss_if(leader, s_t, qx + (((kk >> 2) * Sh::kQPanel + (kk & 3) * 32) >> 4), kx + (((kk >> 2) * Sh::kKPanel + (kk & 3) * 32) >> 4),
+                              idesc_qk, (x > 0 || kk > 0) ? 1u : 0u);
+            }
+            if (leader) {
               tc2_commit_both(bar(kRgSFull + (u & 1)));
-              if (j == g.n - 1) tc2_commit_both(bar(kRgQFree));
+              if (j == n - 1) tc2_commit_both(bar(kRgQFree));
             }
-            if (j > 0) {   // O += P V of tile j - 1
-              const int u = t + j - 1, st = u % kStages;
-              const uint32_t p_t = tmem + 128 * (u & 1);
-#pragma unroll
-              for (int c = 0; c < (kExact ? 1 : 2); ++c) {   // 64 positions; the first P also says that O may be written
-                if (!(ok = bounded_wait(bar((c == 0 ? kRgPFull : kRgPRest) + (u & 1)), (u >> 1) & 1))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int x = 0; x < (kExact ? 3 : 1); ++x) {   // Ph Vh, Pl Vh, Ph Vl
-                  const uint64_t vx = tc_sdesc(sbase + Sh::kVOff + (st * Sh::kParts + (x == 2 ? 1 : 0)) * Sh::kVPart, Sh::kVPanel, 1024);
-#pragma unroll
-                  for (int ks = 4 * c; ks < 4 * c + 4; ++ks)
-                    tc2_mma_ts(tmem + kTmO, p_t + (x == 1 ? 32 : 0) + 8 * ks, vx + ((ks * 16 * 128) >> 4), idesc_pv,
-                               (j > 1 || x > 0 || ks > 0) ? 1u : 0u);
-                }
-              }
-              if (!ok) break;
-              tc2_commit_both(bar(kRgVEmpty + (u & 1)));
-            }
+            __syncwarp();
           }
-          t += g.n;
+          if (j > 0) {   // O += P V of tile j - 1
+            const int u = t + j - 1, st = u % kStages;
+            const uint32_t p_t = tm0 + 128 * (u & 1);
+#pragma unroll
+            for (int c = 0; c < (kExact ? 1 : 2); ++c) {   // 64 positions; the first P also says that O may be written
+              if (!(ok = warp_wait(bar((c == 0 ? kRgPFull : kRgPRest) + (u & 1)), (u >> 1) & 1))) break;
+              tc_fence_after();
+#pragma unroll
+              for (int x = 0; x < (kExact ? 3 : 1); ++x) {   // Ph Vh, Pl Vh, Ph Vl
+                const uint64_t vx = tc_sdesc(sb0 + Sh::kVOff + (st * Sh::kParts + (x == 2 ? 1 : 0)) * Sh::kVPart, Sh::kVPanel, 1024);
+#pragma unroll
+                for (int ks = 4 * c; ks < 4 * c + 4; ++ks)
+                  tc2_mma_ts_if(leader, tm0 + kTmO, p_t + (x == 1 ? 32 : 0) + 8 * ks, vx + ((ks * 16 * 128) >> 4), idesc_pv,
+                                (j > 1 || x > 0 || ks > 0) ? 1u : 0u);
+              }
+            }
+            if (!ok) break;
+            if (leader) tc2_commit_both(bar(kRgVEmpty + (u & 1)));
+            __syncwarp();
+          }
         }
-        // every product that this thread issued has completed before TMEM is released
+        t += n;
+      }
+      if (leader) {   // every product has completed before TMEM is released
         tc2_commit_own(bar(kRgDrain));
         drain(bar(kRgDrain), 0);
       }
