@@ -66,7 +66,22 @@ void lloyd_max_levels(int levels, double sigma, double* c, double* b) {
   }
   for (int j = 0; j + 1 < levels; ++j) b[j] = 0.5 * (c[j] + c[j + 1]);
 }
-void lloyd_max_16(double sigma, double c[16], double b[15]) { lloyd_max_levels(16, sigma, c, b); }
+
+// The format's codebooks (16, 4 and 8 levels), solved once a process: the iterations take 130 ms, and every
+// context has the same ones.
+struct Codebooks {
+  double c[16], b[15];
+  double cb[2][8], bb[2][7];
+};
+const Codebooks& codebooks() {
+  static const Codebooks k = [] {
+    Codebooks x{};
+    lloyd_max_levels(16, 1.0 / 16.0, x.c, x.b);
+    for (int v = 0; v < 2; ++v) lloyd_max_levels(4 << v, 1.0 / 16.0, x.cb[v], x.bb[v]);
+    return x;
+  }();
+  return k;
+}
 
 uint16_t half_bits(double x) {
   const __half h = __double2half(x);
@@ -402,7 +417,11 @@ int tq4_ctx_create(const int8_t* signs, tq4_ctx** out) {
   // midpoints (rounded to fp32), reconstruction reads the centroids rounded to
   // fp32, and the attention kernels read each centroid as an f16 hi + lo pair
   tq4::Codebook cb{};
-  lloyd_max_16(1.0 / 16.0, ctx->centroids, ctx->boundaries);
+  const Codebooks& books = codebooks();
+  std::memcpy(ctx->centroids, books.c, sizeof(books.c));
+  std::memcpy(ctx->boundaries, books.b, sizeof(books.b));
+  std::memcpy(ctx->centroids_b, books.cb, sizeof(books.cb));
+  std::memcpy(ctx->boundaries_b, books.bb, sizeof(books.bb));
   for (int j = 0; j < 16; ++j) {
     cb.c[j] = float(ctx->centroids[j]);
     cb.c16[j] = half_bits(ctx->centroids[j]);
@@ -414,7 +433,6 @@ int tq4_ctx_create(const int8_t* signs, tq4_ctx** out) {
   tq4::CodebookB cbb[2]{};   // the 2- and 3-bit variants, stored the same way
   for (int v = 0; v < 2; ++v) {
     const int levels = 4 << v;
-    lloyd_max_levels(levels, 1.0 / 16.0, ctx->centroids_b[v], ctx->boundaries_b[v]);
     for (int j = 0; j < levels; ++j) {
       cbb[v].c[j] = float(ctx->centroids_b[v][j]);
       cbb[v].c16[j] = half_bits(ctx->centroids_b[v][j]);
@@ -1023,13 +1041,16 @@ int tq4_decode_attention_window(tq4_ctx* ctx, const void* pool, int32_t num_page
 }
 
 size_t tq4_prefill_ragged_workspace_bytes(const tq4_ctx* ctx, int32_t n_req, int32_t n_tok, int32_t max_pages,
-                                          int32_t window, int32_t n_sink, int out_dtype) {
-  if (!ctx || n_req <= 0 || n_tok <= 0 || max_pages <= 0 || window < 1 || n_sink < 0) return 0;
-  return tq4::ragged_layout(ctx->num_sms, n_req, n_tok, max_pages, window, n_sink, out_dtype == TQ4_DTYPE_F32).total;
+                                          int32_t window, int32_t n_sink, int64_t max_positions, int out_dtype) {
+  if (!ctx || n_req <= 0 || n_tok <= 0 || max_pages <= 0 || window < 1 || n_sink < 0 || max_positions < 0) return 0;
+  const bool exact = out_dtype == TQ4_DTYPE_F32;
+  // a request's first and last tiles, and the one after its sinks, may hold rows of no visible position
+  const int64_t rows = max_positions > 0 ? max_positions + int64_t(std::min(n_req, n_tok)) * 4 * (exact ? 64 : 128) : INT64_MAX;
+  return tq4::ragged_layout(ctx->num_sms, n_req, n_tok, max_pages, window, n_sink, exact, rows).total + 2048;
 }
 
 int tq4_prefill_attention_ragged(tq4_ctx* ctx, const void* pool, int32_t num_pages, const uint16_t* q,
-                                 const uint16_t* k_new, const uint16_t* v_new, int32_t n_tok, const int32_t* cu_tok,
+                                 const uint16_t* k_new, const uint16_t* v_new, int64_t k_stride, int64_t v_stride, int32_t n_tok, const int32_t* cu_tok,
                                  const int32_t* seq_lens, const int32_t* page_tables, int32_t max_pages, int32_t n_req,
                                  int32_t window, int32_t n_sink, float scale, void* out, int out_dtype,
                                  void* workspace, size_t workspace_bytes, void* stream) {
@@ -1041,14 +1062,14 @@ int tq4_prefill_attention_ragged(tq4_ctx* ctx, const void* pool, int32_t num_pag
     return TQ4_ERR_ARG;
   if (!aligned(pool, 16) || !aligned(q, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(out, 16))
     return TQ4_ERR_ARG;
+  if (k_stride < tq4::kHkv * tq4::kD || v_stride < tq4::kHkv * tq4::kD || k_stride % 8 || v_stride % 8) return TQ4_ERR_ARG;
+  if (n_req > TQ4_RAGGED_MAX_REQUESTS) return TQ4_ERR_UNSUPPORTED;
   const bool exact = out_dtype == TQ4_DTYPE_F32;
-  const tq4::RgLayout l = tq4::ragged_layout(ctx->num_sms, n_req, n_tok, max_pages, window, n_sink, exact);
+  const tq4::RgLayout l = tq4::ragged_layout_in(workspace_bytes, ctx->num_sms, n_req, n_tok, max_pages, window, n_sink, exact);
+  if (!workspace || l.store_rows < 128 || workspace_bytes < l.total || !aligned(workspace, 256)) return TQ4_ERR_WORKSPACE;
   const int64_t parts = exact ? 2 : 1;
   const int64_t q_rows = parts * tq4::kHq * n_tok, kv_rows = parts * 2 * tq4::kHkv * l.store_rows;
-  if (n_req > TQ4_RAGGED_MAX_REQUESTS || int64_t(max_pages) * tq4::kPage > INT32_MAX || q_rows > INT32_MAX ||
-      kv_rows > INT32_MAX)
-    return TQ4_ERR_UNSUPPORTED;
-  if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256)) return TQ4_ERR_WORKSPACE;
+  if (int64_t(max_pages) * tq4::kPage > INT32_MAX || q_rows > INT32_MAX || kv_rows > INT32_MAX) return TQ4_ERR_UNSUPPORTED;
   if (int rc = check_device(ctx)) return rc;
   char* ws = static_cast<char*>(workspace);
   tq4::RaggedParams p{};
@@ -1065,6 +1086,8 @@ int tq4_prefill_attention_ragged(tq4_ctx* ctx, const void* pool, int32_t num_pag
   p.q = q;
   p.k = k_new;
   p.v = v_new;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
   p.scale = scale;
   p.out = out;
   p.out_dtype = out_dtype;

@@ -104,7 +104,7 @@ struct RgHead {
   int32_t n_pairs;          // pairs with work
   int32_t pad;
 };
-struct RgStart { int32_t head, blk, tile, pad; };
+struct RgStart { int32_t head, blk, tile, left; };   // where a pair's share begins; its tiles
 
 struct RaggedParams {
   const uint8_t* pool;
@@ -118,6 +118,7 @@ struct RaggedParams {
   const uint16_t* q;
   const uint16_t* k;
   const uint16_t* v;
+  int64_t k_stride, v_stride;   // elements between tokens
   float scale;
   void* out;
   int out_dtype;
@@ -148,13 +149,13 @@ struct RgLayout {
   size_t head, req, blk_req, blk_cum, starts, qr, qfac, rows, norms, po, pml, total;
 };
 inline RgLayout ragged_layout(int32_t num_sms, int32_t n_req, int32_t n_tok, int32_t max_pages, int32_t window,
-                              int32_t n_sink, bool exact) {
+                              int32_t n_sink, bool exact, int64_t max_rows = INT64_MAX) {
   RgLayout l{};
   const int64_t tile = exact ? 64 : 128, parts = exact ? 2 : 1, busy = std::min(n_req, n_tok);
   const int64_t most = int64_t(max_pages) * (kPage / tile);
   const int64_t some = (int64_t(n_sink) + tile - 1) / tile + int64_t(window) / tile + 3;
   l.blocks = int64_t(6) * n_tok / 256 + busy;
-  l.store_rows = tile * (busy * std::min(most, some) + (n_tok + tile - 1) / tile);
+  l.store_rows = std::min(tile * (busy * std::min(most, some) + (n_tok + tile - 1) / tile), max_rows / tile * tile);
   size_t at = 0;
   auto take = [&at](size_t bytes) {
     const size_t p = at;
@@ -175,6 +176,17 @@ inline RgLayout ragged_layout(int32_t num_sms, int32_t n_req, int32_t n_tok, int
   l.pml = take(2 * pairs * 256 * 8);
   l.total = at;
   return l;
+}
+
+// The layout of a workspace of this many bytes: fewer rows than a batch may need at most are fine, as long as
+// there are enough for the batch at hand (the prep looks). store_rows = 0: too small for anything.
+inline RgLayout ragged_layout_in(size_t bytes, int32_t num_sms, int32_t n_req, int32_t n_tok, int32_t max_pages, int32_t window,
+                                 int32_t n_sink, bool exact) {
+  const size_t fixed = ragged_layout(num_sms, n_req, n_tok, max_pages, window, n_sink, exact, 0).total + 2048;   // and what rounding adds
+  const size_t row = size_t(exact ? 2 : 1) * 2 * kHkv * kD * 2 + kHkv * 4;
+  const RgLayout all = ragged_layout(num_sms, n_req, n_tok, max_pages, window, n_sink, exact);
+  if (bytes >= all.total) return all;
+  return ragged_layout(num_sms, n_req, n_tok, max_pages, window, n_sink, exact, bytes > fixed ? int64_t((bytes - fixed) / row) : 0);
 }
 
 // the last index i of a[0 .. n - 1] (non-decreasing) with a[i] <= x; a[0] <= x
@@ -342,6 +354,11 @@ __global__ void __launch_bounds__(kRgPrepThreads, 2) ragged_prep_kernel(const __
   __shared__ uint32_t pair_s[256][8];   // centroid pairs of a byte of codes, f16 hi: 8 copies against bank conflicts
   __shared__ uint32_t res_s[kExact ? 256 : 1][8];   // and lo
   __shared__ int32_t s_blocks, s_tiles;
+  // the layout of a small batch, near at hand for the bisections
+  constexpr int kNearReq = 64, kNearBlocks = 768;
+  __shared__ RgReq req_s[kNearReq];
+  __shared__ int64_t cum_s[kNearBlocks + 1];
+  RgReq* const req = p.n_req <= kNearReq ? req_s : p.req;
   int32_t* const row0_s = prep_smem;             // [n_req]
   int32_t* const tile0_s = row0_s + p.n_req;     // [n_req]
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -354,6 +371,7 @@ __global__ void __launch_bounds__(kRgPrepThreads, 2) ragged_prep_kernel(const __
     }
   }
   if (tid < 3) carry[tid] = 0;
+  if (tid == 0) s_blocks = s_tiles = 0;
   pdl_wait();
   pdl_launch_dependents();
   __syncthreads();
@@ -408,24 +426,35 @@ __global__ void __launch_bounds__(kRgPrepThreads, 2) ragged_prep_kernel(const __
     }
     if (r < p.n_req) {
       row0_s[r] = int32_t(min(int64_t(cu0) + before, int64_t(INT32_MAX)));
-      tile0_s[r] = int32_t(tile0);
+      if (tiles > 0) {   // a request whose rows do not fit the workspace is refused, and so are those with work after it
+        if ((tile0 + tiles) * kTile <= p.store_rows) {
+          atomicMax(&s_blocks, int32_t(blk0 + blocks));
+          atomicMax(&s_tiles, int32_t(tile0 + tiles));
+        } else {
+          if (blockIdx.x == 0) record_error(p.status, TQ4_ERR_WORKSPACE);
+          tile0 = INT32_MAX;
+          rq.n_new = 0;
+        }
+      }
+      tile0_s[r] = int32_t(min(tile0, int64_t(INT32_MAX)));
       rq.tile0 = int32_t(tile0);
       rq.blk0 = int32_t(blk0);
-      if (blockIdx.x == 0) p.req[r] = rq;
+      if (blockIdx.x == 0) {
+        p.req[r] = rq;
+        if (p.n_req <= kNearReq) req_s[r] = rq;
+      }
     }
     __syncthreads();
     if (tid < 3)
       for (int x = 0; x < kRgPrepThreads / 32; ++x) carry[tid] += tot[tid][x];
     __syncthreads();
   }
-  if (tid == 0) {
-    s_blocks = int32_t(carry[1]);
-    s_tiles = int32_t(carry[2]);
-  }
   __syncthreads();
 
   if (blockIdx.x == 0) {
     // ---- tiles of each row block, their running sum, and the pairs' shares
+    const bool near = s_blocks <= kNearBlocks;
+    int64_t* const cum = near ? cum_s : p.blk_cum;
     if (tid == 0) carry[0] = 0;
     __syncthreads();
     for (int base = 0; base < s_blocks; base += kRgPrepThreads) {
@@ -435,11 +464,11 @@ __global__ void __launch_bounds__(kRgPrepThreads, 2) ragged_prep_kernel(const __
         int lo = 0, hi = p.n_req - 1;   // the last request whose first block is at or before i
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
-          if (p.req[mid].blk0 <= i) lo = mid;
+          if (req[mid].blk0 <= i) lo = mid;
           else hi = mid - 1;
         }
         p.blk_req[i] = lo;
-        const RgReq rq = p.req[lo];
+        const RgReq rq = req[lo];
         n = rg_block_span<kTile>(p, rq, i - rq.blk0).n;
       }
       const int64_t sum = warp_scan_i64(n);
@@ -447,7 +476,10 @@ __global__ void __launch_bounds__(kRgPrepThreads, 2) ragged_prep_kernel(const __
       __syncthreads();
       int64_t before = carry[0] + sum - n;
       for (int x = 0; x < w; ++x) before += tot[0][x];
-      if (i < s_blocks) p.blk_cum[i] = before;
+      if (i < s_blocks) {
+        p.blk_cum[i] = before;
+        if (near) cum_s[i] = before;
+      }
       __syncthreads();
       if (tid == 0)
         for (int x = 0; x < kRgPrepThreads / 32; ++x) carry[0] += tot[0][x];
@@ -462,18 +494,29 @@ __global__ void __launch_bounds__(kRgPrepThreads, 2) ragged_prep_kernel(const __
     const int pairs = int(min(int64_t(p.max_pairs), all > 0 ? max(cost / (kMin + extra), int64_t(1)) : int64_t(0)));
     if (tid == 0) {
       p.blk_cum[s_blocks] = per_head;
+      if (near) cum_s[s_blocks] = per_head;
       *p.head = RgHead{s_blocks, s_tiles, pairs, 0};
     }
     __syncthreads();
-    for (int s = tid; s < pairs; s += kRgPrepThreads) {
-      const int64_t g = int64_t(s) * cost / pairs, head = g / cost_head, at = g - head * cost_head;
-      int lo = 0, hi = s_blocks - 1;   // the last block whose cost begins at or before `at`
+    // where share x begins, and the tiles before it
+    auto start = [&](int x, RgStart& at) -> int64_t {
+      if (x == pairs) return all;
+      const int64_t g = int64_t(x) * cost / pairs, head = g / cost_head, in = g - head * cost_head;
+      int lo = 0, hi = s_blocks - 1;   // the last block whose cost begins at or before `in`
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.blk_cum[mid] + extra * mid <= at) lo = mid;
+        if (cum[mid] + extra * mid <= in) lo = mid;
         else hi = mid - 1;
       }
-      p.starts[s] = RgStart{int32_t(head), lo, int32_t(max(at - p.blk_cum[lo] - extra * (lo + 1), int64_t(0))), 0};
+      const int64_t tile = max(in - cum[lo] - extra * (lo + 1), int64_t(0));
+      at = RgStart{int32_t(head), lo, int32_t(tile), 0};
+      return head * per_head + cum[lo] + tile;
+    };
+    for (int x = tid; x < pairs; x += kRgPrepThreads) {
+      RgStart at, next;
+      const int64_t begin = start(x, at);
+      at.left = int32_t(start(x + 1, next) - begin);
+      p.starts[x] = at;
     }
     return;
   }
@@ -499,7 +542,7 @@ __global__ void __launch_bounds__(kRgPrepThreads, 2) ragged_prep_kernel(const __
       const int64_t off = (int64_t(tok) * kHq + hq) * kD + at8;
       const int r = rg_last_at_most<int32_t>(row0_s, p.n_req, tok);
       const int32_t T = p.seq_lens[r], a = p.cu[r], b = p.cu[r + 1];
-      const bool work = a >= 0 && a == row0_s[r] && b <= p.n_tok && tok >= a && tok < b && T > 0 &&
+      const bool work = a >= 0 && a == row0_s[r] && tile0_s[r] < INT32_MAX && b <= p.n_tok && tok >= a && tok < b && T > 0 &&
                         int64_t(T) <= int64_t(p.max_pages) * kPage && T >= b - a;
       if (!work) {   // a refused request: zeros
         const uint4 z = make_uint4(0, 0, 0, 0);
@@ -542,12 +585,12 @@ __global__ void __launch_bounds__(kRgPrepThreads, 2) ragged_prep_kernel(const __
     if (pos0 + 3 >= first && pos0 < T) {   // the chunk's own are among them: eight lanes each
       const int32_t pos = pos0 + sub;
       const bool mine = pos >= first && pos < T;
-      const int64_t off = (int64_t(row0 + pos - first) * kHkv + h) * kD + at8;
+      const int64_t tok = row0 + pos - first, at = h * kD + at8;
       uint4 raw_k[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        raw[c] = mine ? __ldg(reinterpret_cast<const uint4*>(p.v + off + 64 * c)) : make_uint4(0, 0, 0, 0);
-        raw_k[c] = mine ? __ldg(reinterpret_cast<const uint4*>(p.k + off + 64 * c)) : make_uint4(0, 0, 0, 0);
+        raw[c] = mine ? __ldg(reinterpret_cast<const uint4*>(p.v + tok * p.v_stride + at + 64 * c)) : make_uint4(0, 0, 0, 0);
+        raw_k[c] = mine ? __ldg(reinterpret_cast<const uint4*>(p.k + tok * p.k_stride + at + 64 * c)) : make_uint4(0, 0, 0, 0);
       }
       const uint32_t vtop = rg_rotate4(raw, mask, vec);
       const bool v_fits = vtop <= kRgTop;
@@ -680,21 +723,13 @@ static_assert(sizeof(RgItem) <= 64, "item records");
 // The pair's stretches in order; every warp walks them by itself.
 struct RgWalk {
   const RaggedParams& p;
-  int pair, n_blk;
-  int64_t left;
+  int pair, n_blk, left;
   int32_t head, blk, tile;
   bool first;
   __device__ __forceinline__ RgWalk(const RaggedParams& params, int pr) : p(params), pair(pr) {
-    const RgHead hd = *p.head;
-    n_blk = hd.n_blk;
-    const int64_t per_head = p.blk_cum[n_blk];
+    n_blk = p.head->n_blk;
     const RgStart s = p.starts[pair];
-    int64_t end = per_head * kHkv;   // tiles before the next pair's share
-    if (pair + 1 < hd.n_pairs) {
-      const RgStart e = p.starts[pair + 1];
-      end = e.head * per_head + p.blk_cum[e.blk] + e.tile;
-    }
-    left = end - (s.head * per_head + p.blk_cum[s.blk] + s.tile);
+    left = s.left;
     head = s.head;
     blk = s.blk;
     tile = s.tile;
@@ -706,7 +741,7 @@ struct RgWalk {
     g.blk = blk;
     g.tile = tile;
     g.all = int32_t(p.blk_cum[blk + 1] - p.blk_cum[blk]);
-    g.n = int32_t(min(int64_t(g.all - tile), left));
+    g.n = min(g.all - tile, left);
     g.part = g.n == g.all ? -1 : 2 * pair + (first ? 0 : 1);
     left -= g.n;
     first = false;
@@ -866,7 +901,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRgThreads, 1)
       const uint32_t lane_addr = tmem + (uint32_t(32 * quad) << 16);
       const float* norms = reinterpret_cast<const float*>(smem + Sh::kNormOff) + 32 * half;
       int t = 0;      // tiles of this pair so far
-      int64_t left = walk.left;
+      int left = walk.left;
       bool ok = true;
       // The two warps of these rows swap a value per row through buf and agree on going on, so that after a wait
       // that gave up both leave at the same meeting (the value is then kRgGone).

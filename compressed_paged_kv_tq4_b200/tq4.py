@@ -7,6 +7,7 @@ raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -133,8 +134,8 @@ _sig = {
     "tq4_decode_window_workspace_bytes": ([_p, _i32, _i32, _i32, _i32, _i32], _sz),
     "tq4_decode_attention_window": ([_p, _p, _i32, _p, _p, _i32, _p, _i32, _i32, _i32, _i32, _f, _p, ctypes.c_int,
                                      _p, _sz, _p], ctypes.c_int),
-    "tq4_prefill_ragged_workspace_bytes": ([_p, _i32, _i32, _i32, _i32, _i32, ctypes.c_int], _sz),
-    "tq4_prefill_attention_ragged": ([_p, _p, _i32, _p, _p, _p, _i32, _p, _p, _p, _i32, _i32, _i32, _i32, _f, _p,
+    "tq4_prefill_ragged_workspace_bytes": ([_p, _i32, _i32, _i32, _i32, _i32, _i64, ctypes.c_int], _sz),
+    "tq4_prefill_attention_ragged": ([_p, _p, _i32, _p, _p, _p, _i64, _i64, _i32, _p, _p, _p, _i32, _i32, _i32, _i32, _f, _p,
                                       ctypes.c_int, _p, _sz, _p], ctypes.c_int),
     "tq4_pages_create": ([_i32, ctypes.POINTER(_p)], ctypes.c_int),
     "tq4_pages_destroy": ([_p], ctypes.c_int),
@@ -389,15 +390,15 @@ def tq4_decode_attention_window(ctx, pool, num_pages, q, page_tables, max_pages,
                                             _ptr(workspace), workspace_bytes, _stream(stream))
 
 
-def tq4_prefill_ragged_workspace_bytes(ctx, n_req, n_tok, max_pages, window, n_sink, out_dtype) -> int:
-    return _lib.tq4_prefill_ragged_workspace_bytes(ctx, n_req, n_tok, max_pages, window, n_sink, out_dtype)
+def tq4_prefill_ragged_workspace_bytes(ctx, n_req, n_tok, max_pages, window, n_sink, max_positions, out_dtype) -> int:
+    return _lib.tq4_prefill_ragged_workspace_bytes(ctx, n_req, n_tok, max_pages, window, n_sink, max_positions, out_dtype)
 
 
-def tq4_prefill_attention_ragged(ctx, pool, num_pages, q, k_new, v_new, n_tok, cu_tok, seq_lens, page_tables, max_pages,
-                                 n_req, window, n_sink, scale, out, out_dtype, workspace, workspace_bytes,
+def tq4_prefill_attention_ragged(ctx, pool, num_pages, q, k_new, v_new, k_stride, v_stride, n_tok, cu_tok, seq_lens,
+                                 page_tables, max_pages, n_req, window, n_sink, scale, out, out_dtype, workspace, workspace_bytes,
                                  stream=None) -> int:
-    return _lib.tq4_prefill_attention_ragged(ctx, _ptr(pool), num_pages, _ptr(q), _ptr(k_new), _ptr(v_new), n_tok,
-                                             _ptr(cu_tok), _ptr(seq_lens), _ptr(page_tables), max_pages, n_req, window,
+    return _lib.tq4_prefill_attention_ragged(ctx, _ptr(pool), num_pages, _ptr(q), _ptr(k_new), _ptr(v_new), k_stride,
+                                             v_stride, n_tok, _ptr(cu_tok), _ptr(seq_lens), _ptr(page_tables), max_pages, n_req, window,
                                              n_sink, scale, _ptr(out), out_dtype, _ptr(workspace), workspace_bytes,
                                              _stream(stream))
 
@@ -559,6 +560,19 @@ def _refuse(name, t, dtypes, shape, device, rows):
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     if not (rows and t[:1].is_contiguous()) and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _allocating(stream):
+    """Tensors made in this context belong to the call's stream, so that a scratch freed after the call is not
+    given away while the call runs, and what is filled here is filled before it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream))
+
+
+def _need_window(window, sinks):
+    if not (0 < window < 1 << 31 and 0 <= sinks < 1 << 31):
+        raise ValueError(f"a window of {window} with {sinks} sinks")
 
 
 def _out_code(out):
@@ -958,7 +972,8 @@ class Context:
         if q is not None:
             _need_rows("q", q, dtype, (n, Q_HEADS, HEAD_DIM), dev)
             if q_out is None:
-                q_out = torch.empty((n, Q_HEADS, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+                with _allocating(stream):
+                    q_out = torch.empty((n, Q_HEADS, HEAD_DIM), dtype=torch.bfloat16, device=dev)
             _need("q_out", q_out, torch.bfloat16, (n, Q_HEADS, HEAD_DIM), dev)
         elif q_out is not None:
             raise ValueError("q_out without q")
@@ -988,8 +1003,9 @@ class Context:
         n = slots.numel()
         num_pages = _pool_pages(pool, self.device)
         _need("slots", slots, torch.int64, (n,), self.device)
-        k = torch.empty((n, KV_HEADS, HEAD_DIM), dtype=out_dtype, device=self.device)
-        v = torch.empty_like(k)
+        with _allocating(stream):
+            k = torch.empty((n, KV_HEADS, HEAD_DIM), dtype=out_dtype, device=self.device)
+            v = torch.empty_like(k)
         _check(_lib.tq4_reconstruct_slots(self.handle, pool.data_ptr(), num_pages, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
                                           code, self._stream(stream)), "tq4_reconstruct_slots")
         return k, v
@@ -1009,21 +1025,26 @@ class Context:
         _need("q", q, torch.bfloat16, shape, dev)
         _need("page_tables", page_tables, torch.int32, (n_req, max_pages), dev)
         _need("seq_lens", seq_lens, torch.int32, (n_req,), dev)
-        if out is None:
-            out = torch.empty(shape, dtype=out_dtype, device=dev)
+        _need_window(window, sinks)
+        if out is None or workspace is None:
+            with _allocating(stream):
+                if out is None:
+                    out = torch.empty(shape, dtype=out_dtype, device=dev)
+                if workspace is None and n_req > 0:
+                    workspace = self.decode_window_workspace(n_req, n_q, max_pages, window, sinks, dev)
         code = _out_code(out)
         _need("out", out, out.dtype, shape, dev)
-        if workspace is None and n_req > 0:
-            workspace = self.decode_window_workspace(n_req, n_q, max_pages, window, sinks, dev)
         _check(_lib.tq4_decode_attention_window(self.handle, pool.data_ptr(), num_pages, q.data_ptr(), page_tables.data_ptr(),
                                                 max_pages, seq_lens.data_ptr(), n_req, n_q, window, sinks, scale, out.data_ptr(),
                                                 code, *_scratch(workspace, dev), self._stream(stream)), "tq4_decode_attention_window")
         return out
 
     def prefill_ragged_workspace(self, n_req, n_tok, max_pages, window, sinks, out_dtype=torch.float32,
-                                 device="cuda") -> torch.Tensor:
-        """Scratch of prefill_attention_ragged; the default out_dtype's serves both."""
-        nbytes = tq4_prefill_ragged_workspace_bytes(self.handle, n_req, n_tok, max_pages, window, sinks,
+                                 device="cuda", max_positions=0) -> torch.Tensor:
+        """Scratch of prefill_attention_ragged; the default out_dtype's serves both. max_positions: an upper
+        bound on the visible positions of all requests together (0: whatever tables, window and sinks allow)."""
+        _need_window(window, sinks)
+        nbytes = tq4_prefill_ragged_workspace_bytes(self.handle, n_req, n_tok, max_pages, window, sinks, max_positions,
                                                     _OUT_CODES[out_dtype])
         return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
@@ -1031,24 +1052,30 @@ class Context:
                                  out=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
         """Chunks of several requests over their paged prefixes: q bf16 [rows, 24, 256], k_new, v_new bf16
         [rows, 4, 256] (request r's rows are cu_tok[r] .. cu_tok[r + 1] - 1), seq_lens int32 [n_req] with the new
-        positions, page_tables int32 [n_req, max_pages]. Rows behind the last request's are left as they were."""
+        positions, page_tables int32 [n_req, max_pages]; k_new, v_new may be slices of a projection. Rows behind the last request's are left as they were."""
         dev, rows, n_req = self.device, q.shape[0], seq_lens.numel()
         shape, kv_shape, max_pages = (rows, Q_HEADS, HEAD_DIM), (rows, KV_HEADS, HEAD_DIM), page_tables.shape[-1]
         num_pages = _pool_pages(pool, dev)
         _need("q", q, torch.bfloat16, shape, dev)
-        _need("k_new", k_new, torch.bfloat16, kv_shape, dev)
-        _need("v_new", v_new, torch.bfloat16, kv_shape, dev)
+        _need_rows("k_new", k_new, torch.bfloat16, kv_shape, dev)
+        _need_rows("v_new", v_new, torch.bfloat16, kv_shape, dev)
         _need("cu_tok", cu_tok, torch.int32, (n_req + 1,), dev)
         _need("seq_lens", seq_lens, torch.int32, (n_req,), dev)
         _need("page_tables", page_tables, torch.int32, (n_req, max_pages), dev)
-        if out is None:
-            out = torch.zeros(shape, dtype=out_dtype, device=dev)
+        _need_window(window, sinks)
+        if out is None or workspace is None:
+            with _allocating(stream):
+                if out is None:
+                    out = torch.zeros(shape, dtype=out_dtype, device=dev)
+                _out_code(out)
+                if workspace is None and n_req > 0 and rows > 0:
+                    workspace = self.prefill_ragged_workspace(n_req, rows, max_pages, window, sinks, out.dtype, dev)
         code = _out_code(out)
         _need("out", out, out.dtype, shape, dev)
-        if workspace is None and n_req > 0 and rows > 0:
-            workspace = self.prefill_ragged_workspace(n_req, rows, max_pages, window, sinks, out.dtype, dev)
         _check(_lib.tq4_prefill_attention_ragged(self.handle, pool.data_ptr(), num_pages, q.data_ptr(), k_new.data_ptr(),
-                                                 v_new.data_ptr(), rows, cu_tok.data_ptr(), seq_lens.data_ptr(),
+                                                 v_new.data_ptr(), k_new.stride(0) if rows > 1 else KV_HEADS * HEAD_DIM,
+                                                 v_new.stride(0) if rows > 1 else KV_HEADS * HEAD_DIM, rows,
+                                                 cu_tok.data_ptr(), seq_lens.data_ptr(),
                                                  page_tables.data_ptr(), max_pages, n_req, window, sinks, scale, out.data_ptr(),
                                                  code, *_scratch(workspace, dev), self._stream(stream)),
                "tq4_prefill_attention_ragged")

@@ -270,7 +270,9 @@ int tq4_prefill_attention_reconstructed(tq4_ctx* ctx, const void* pool, int32_t 
  *                    tensor-memory decode of 2-4 tokens does not signal the
  *                    tensor-core issuer that the first key chunk is ready; the
  *                    prefill kernel does not signal it that P of tile
- *                    min(1, tiles - 1) is ready); their results are
+ *                    min(1, tiles - 1) is ready; the windowed decode is as the
+ *                    one-token decode, the ragged prefill as the prefill with
+ *                    each CTA pair's first two tiles); their results are
  *                    then undefined and the status is TQ4_ERR_TIMEOUT. 0 (the
  *                    default) restores normal operation.
  * Returns TQ4_ERR_ARG for a NULL context. */
@@ -504,13 +506,14 @@ int tq4_reconstruct_slots(tq4_ctx* ctx, const void* pool, int32_t num_pages, con
 /* Decode attention with a sliding window and sinks: as tq4_decode_attention, but query
  * token t of a request, at position P = seq_len - n_q + t, sees the positions j <= P
  * with j > P - window or j < n_sink. Only the pages that hold such positions are read
- * (entries of others may be anything). One launch. A request of length 0 (refused, or
+ * (entries of others may be anything). A request of length 0 (refused, or
  * padding of the batch) gives zeros; a length below n_q or past the table gives zeros and
  * records TQ4_ERR_SEQ. window >= 1; a window of the whole history is the plain decode.
  * bf16 results carry the queries, the centroids and the weights as single f16 operands
  * (each rounded once, relative 2^-11); fp32 results as hi + lo pairs.
  *   workspace    device, at least tq4_decode_window_workspace_bytes(...) bytes, 256-B
- *                aligned; NULL where that is 0. */
+ *                aligned; NULL where that is 0 (few requests: one launch). Calls that may
+ *                overlap need one each. */
 size_t tq4_decode_window_workspace_bytes(const tq4_ctx* ctx, int32_t n_req, int32_t n_q,
                                          int32_t max_pages, int32_t window, int32_t n_sink);
 int tq4_decode_attention_window(tq4_ctx* ctx, const void* pool, int32_t num_pages,
@@ -526,7 +529,8 @@ int tq4_decode_attention_window(tq4_ctx* ctx, const void* pool, int32_t num_page
  * before the chunk from the cache, the chunk's own from k_new and v_new (as
  * tq4_prefill_attention; whether the chunk has been appended does not matter).
  *   q            device bf16 [n_tok][24][256]
- *   k_new, v_new device bf16 [n_tok][4][256]
+ *   k_new, v_new device bf16: token rows of [4][256], k_stride and v_stride elements apart
+ *                (slices of a projection are fine), 16-B aligned
  *   cu_tok       device int32 [n_req + 1], non-decreasing, at most n_tok
  *   seq_lens     device int32 [n_req], positions INCLUDING the new ones
  *   page_tables  device int32 [n_req][max_pages]; only the entries of pages that some
@@ -534,25 +538,26 @@ int tq4_decode_attention_window(tq4_ctx* ctx, const void* pool, int32_t num_page
  *   out          device [n_tok][24][256], out_dtype. Rows before cu_tok[0] and behind the
  *                last request's are left as they were; those of a request of length 0
  *                (refused) are zeros.
- *   workspace    device, tq4_prefill_ragged_workspace_bytes(...) bytes (same arguments and
- *                out_dtype), 256-B aligned. Calls that may overlap need one each.
+ *   workspace    device, 256-B aligned; calls that may overlap need one each. It holds one f16
+ *                row (fp32: two) per visible position, KV head, K and V: 4 KiB (8 KiB) a
+ *                position. tq4_prefill_ragged_workspace_bytes gives what any lengths can need
+ *                (max_positions 0), or what suffices while the visible positions of all
+ *                requests number at most max_positions; a request whose rows do not fit, and
+ *                those with new tokens after it, get zeros and TQ4_ERR_WORKSPACE is recorded.
  * A request whose rows or length are inconsistent (cu_tok out of order or past n_tok, a
  * length below its tokens or past the table) gets zeros where its rows are its own, and
  * TQ4_ERR_SEQ is recorded. bf16 results carry the operands as single f16 values (each
  * rounded once, relative 2^-11), fp32 results as hi + lo pairs. A vector with an infinity
  * or a NaN (in the chunk also one with a rotated coordinate of 32,768 or more, which the
  * cache's fp16 norm hardly holds either) makes the results of those who see it NaN, of no
- * other. At most
- * TQ4_RAGGED_MAX_REQUESTS requests. The workspace holds one f16 row (fp32: two) per visible
- * position, KV head, K and V: 4 KiB (8 KiB) a position, for at most sinks + window + new
- * positions of each request. */
+ * other. At most TQ4_RAGGED_MAX_REQUESTS requests. */
 #define TQ4_RAGGED_MAX_REQUESTS 16384
 size_t tq4_prefill_ragged_workspace_bytes(const tq4_ctx* ctx, int32_t n_req, int32_t n_tok,
                                           int32_t max_pages, int32_t window, int32_t n_sink,
-                                          int out_dtype);
+                                          int64_t max_positions, int out_dtype);
 int tq4_prefill_attention_ragged(tq4_ctx* ctx, const void* pool, int32_t num_pages, const uint16_t* q,
-                                 const uint16_t* k_new, const uint16_t* v_new, int32_t n_tok,
-                                 const int32_t* cu_tok, const int32_t* seq_lens,
+                                 const uint16_t* k_new, const uint16_t* v_new, int64_t k_stride,
+                                 int64_t v_stride, int32_t n_tok, const int32_t* cu_tok, const int32_t* seq_lens,
                                  const int32_t* page_tables, int32_t max_pages, int32_t n_req,
                                  int32_t window, int32_t n_sink, float scale, void* out, int out_dtype,
                                  void* workspace, size_t workspace_bytes, void* stream);

@@ -201,6 +201,46 @@ def test_captured_and_replayed_with_other_lengths(ctx):
     assert ctx.status() == tq4.TQ4_OK
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_workspace_for_the_positions_at_hand(ctx, dtype):
+    """Tables of 40 pages, but 1,030 visible positions in all; then a batch whose last requests do not fit."""
+    rng, lens, tab, pool, cu, q, k, v = _case([500, 0, 300, 40], [30, 100, 50, 10], seed=15)
+    wide = np.full((4, 40), -1, np.int32)
+    wide[:, :tab.shape[1]] = tab
+    exp = _oracle(pool, tab, lens, cu, q, k, v, BIG, 0)
+    ws = ctx.prefill_ragged_workspace(4, 190, 40, BIG, 0, dtype, max_positions=1030)
+    assert ws.numel() < ctx.prefill_ragged_workspace(4, 190, 40, BIG, 0, dtype).numel() / 2
+    dev = [torch.from_numpy(pool).cuda(), q.cuda(), k.cuda(), v.cuda(), _i32(cu)]
+    out = ctx.prefill_attention_ragged(*dev, _i32(lens), _i32(wide), BIG, 0, SCALE, out_dtype=dtype, workspace=ws)
+    torch.cuda.synchronize()
+    assert ctx.status() == tq4.TQ4_OK
+    assert_close(out, exp)
+    small = ctx.prefill_ragged_workspace(1, 190, 40, BIG, 0, dtype, max_positions=640)
+    out = ctx.prefill_attention_ragged(*dev, _i32(lens), _i32(wide), BIG, 0, SCALE, out_dtype=dtype, workspace=small)
+    torch.cuda.synchronize()
+    assert ctx.status() == tq4.TQ4_ERR_WORKSPACE
+    assert_close(out[:30], exp[:30])
+    host = out.double().cpu().numpy()
+    assert not host[180:].any()   # zeros from the first request that does not fit on
+    for a, b in ((30, 130), (130, 180)):
+        assert not host[a:b].any() or np.abs(host[a:b] - exp[a:b]).max() <= 0.02
+
+
+def test_another_stream_allocates_for_itself(ctx):
+    rng, lens, tab, pool, cu, q, k, v = _case([300, 20], [40, 30], seed=16)
+    dev = [torch.from_numpy(pool).cuda(), q.cuda(), k.cuda(), v.cuda(), _i32(cu), _i32(lens), _i32(tab)]
+    exp = _oracle(pool, tab, lens, cu, q, k, v, 100, 2)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    outs = []
+    for stream in (s, s.cuda_stream):
+        outs.append(ctx.prefill_attention_ragged(*dev, 100, 2, SCALE, out_dtype=torch.float32, stream=stream))
+        torch.empty(1 << 26, dtype=torch.uint8, device="cuda").fill_(255)   # the current stream takes freed memory
+    torch.cuda.synchronize()
+    for out in outs:
+        assert_close(out, exp)
+
+
 def test_repeats_bit_for_bit(ctx):
     a = _run(ctx, [900, 20], [100, 70], 400, 3, torch.bfloat16, seed=11)
     s = torch.cuda.Stream()
@@ -226,9 +266,9 @@ def test_refusals(ctx):
     rng, lens, tab, pool, cu, q, k, v = _case([10], [4], seed=13)
     ok = dict(pool=torch.from_numpy(pool).cuda(), q=q.cuda(), k_new=k.cuda(), v_new=v.cuda(), cu_tok=_i32(cu), seq_lens=_i32(lens),
               page_tables=_i32(tab), window=4, sinks=0, scale=SCALE)
-    for bad, err in ((dict(window=0), tq4.TQ4Error), (dict(sinks=-1), tq4.TQ4Error), (dict(scale=float("nan")), tq4.TQ4Error),
+    for bad, err in ((dict(window=0), ValueError), (dict(sinks=-1), ValueError), (dict(scale=float("nan")), tq4.TQ4Error),
                      (dict(q=q.cuda().float()), ValueError), (dict(k_new=k.cuda()[:3]), ValueError), (dict(cu_tok=_i32([0])), ValueError),
-                     (dict(v_new=v.cuda().transpose(0, 1).contiguous().transpose(0, 1)), ValueError), (dict(seq_lens=_i32(lens).cpu()), ValueError),
+                     (dict(v_new=v.cuda().transpose(1, 2).contiguous().transpose(1, 2)), ValueError), (dict(window=1 << 32), ValueError), (dict(seq_lens=_i32(lens).cpu()), ValueError),
                      (dict(out=torch.zeros(q.shape, device="cuda", dtype=torch.float16)), ValueError),
                      (dict(workspace=torch.empty(512, dtype=torch.uint8, device="cuda")), tq4.TQ4Error)):
         with pytest.raises(err):
@@ -271,7 +311,7 @@ def test_a_run_of_the_step(ctx):
         cs = cs_all[axes[S.rope_axes(rot // 2, sections, False)].T, np.arange(rot // 2)]
         S.store(opool, slot, S.rope_turn(k.double().numpy(), cs[..., 0], cs[..., 1], False), v.double().numpy(), signs, c)
         assert np.array_equal(pool.cpu().numpy(), opool)
-        out = ctx.prefill_attention_ragged(pool, qr, kr, dv.contiguous(), got[0], got[1], dtab, window, sinks, SCALE, out_dtype=torch.float32, workspace=ws)
+        out = ctx.prefill_attention_ragged(pool, qr, kr, dv, got[0], got[1], dtab, window, sinks, SCALE, out_dtype=torch.float32, workspace=ws)
         torch.cuda.synchronize()
         assert ctx.status() == tq4.TQ4_OK
         exp = S.prefill_attention_ragged(opool, tab, lens, cu, qr.double().cpu().numpy(), kr.double().cpu().numpy(), v.double().numpy(), window, sinks,

@@ -265,7 +265,7 @@ def test_wait_that_runs_out_is_reported_and_the_context_recovers(ctx):
 def test_refusals(ctx):
     pool, q = tq4.Context.new_pool(1), torch.zeros((1, 1, 24, 256), dtype=torch.bfloat16, device="cuda")
     tab, lens = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
-    for kw, err in ((dict(window=0), tq4.TQ4Error), (dict(sinks=-1), tq4.TQ4Error), (dict(scale=float("inf")), tq4.TQ4Error),
+    for kw, err in ((dict(window=0), ValueError), (dict(sinks=-1), ValueError), (dict(window=1 << 32), ValueError), (dict(scale=float("inf")), tq4.TQ4Error),
                     (dict(q=q.float()), ValueError), (dict(seq_lens=lens.long()), ValueError), (dict(page_tables=tab.cpu()), ValueError),
                     (dict(q=torch.zeros((1, 5, 24, 256), dtype=torch.bfloat16, device="cuda")), tq4.TQ4Error),
                     (dict(out=torch.zeros((1, 1, 24, 256), dtype=torch.float16, device="cuda")), ValueError),
