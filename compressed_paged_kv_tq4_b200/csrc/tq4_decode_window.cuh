@@ -905,32 +905,38 @@ __global__ void __launch_bounds__(32 * kQ1Warps) decode_window_combine_kernel(co
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, b = int(blockIdx.x) + 1;
   pdl_wait();
   pdl_launch_dependents();
+  // parts b, b + 1, ... begin inside the item: a warp looks at 32 of them at once
   const int n_cta = p.head[0];
+  const int4 prev = p.starts[min(b, p.num_sms) - 1], at = p.starts[min(b + lane, p.num_sms - 1)];
   if (b >= n_cta) return;
-  const int4 me = p.starts[b], prev = p.starts[b - 1];
-  if (me.z == 0) return;                                               // no item is cut here
-  const bool same = prev.x == me.x && prev.y == me.y;
+  const int me_h = __shfl_sync(0xffffffffu, at.x, 0), me_r = __shfl_sync(0xffffffffu, at.y, 0);
+  if (__shfl_sync(0xffffffffu, at.z, 0) == 0) return;                  // no item is cut here
+  const bool same = prev.x == me_h && prev.y == me_r;
   if (same && prev.z > 0) return;                                      // not its first cut
-  const int part0 = 2 * (b - 1) + (same ? 0 : 1);
-  auto more = [&](int i) {   // part i begins inside the item
-    if (i >= n_cta) return false;
-    const int4 s = p.starts[i];
-    return s.x == me.x && s.y == me.y;
-  };
+  const int64_t part0 = 2 * (b - 1) + (same ? 0 : 1);
+  int run = 0;
+  for (int i = b;; i += 32) {
+    const int4 x = i == b ? at : p.starts[min(i + lane, p.num_sms - 1)];
+    const uint32_t in = __ballot_sync(0xffffffffu, i + lane < n_cta && x.x == me_h && x.y == me_r);
+    run += in == 0xffffffffu ? 32 : __ffs(~in) - 1;
+    if (in != 0xffffffffu) break;
+  }
   const uint32_t sb = lane_sign_bits(p.signs);
-  const int64_t out_row0 = int64_t(me.y) * p.n_q * kHq + me.x * kGroup;
+  const int64_t out_row0 = int64_t(me_r) * p.n_q * kHq + me_h * kGroup;
   for (int row = w; row < kGroup * p.n_q; row += kQ1Warps) {
-    float M = p.pml[int64_t(part0) * 24 + row].x;
-    for (int i = b; more(i); ++i) M = fmaxf(M, p.pml[int64_t(2 * i) * 24 + row].x);
+    float M = p.pml[part0 * 24 + row].x;
+#pragma unroll 4
+    for (int i = 0; i < run; ++i) M = fmaxf(M, p.pml[int64_t(2 * (b + i)) * 24 + row].x);
     float L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int i = b - 1; i < b || more(i); ++i) {
-      const int64_t rec = int64_t(i < b ? part0 : 2 * i) * 24 + row;
+#pragma unroll 2
+    for (int i = -1; i < run; ++i) {
+      const int64_t rec = (i < 0 ? part0 : int64_t(2 * (b + i))) * 24 + row;
       const float2 ml = p.pml[rec];
-      if (ml.x == -INFINITY && ml.y == 0.f) continue;   // that part showed this row nothing
-      const float f = fast_exp2(ml.x - M);
-      L = fmaf(f, ml.y, L);
       const float4* src = reinterpret_cast<const float4*>(p.po + rec * kD + lane * 8);
       const float4 x = src[0], y = src[1];
+      const bool seen = ml.x != -INFINITY || ml.y != 0.f;   // else that part showed this row nothing, and its sums are zeros
+      const float f = seen ? fast_exp2(ml.x - M) : 0.f;
+      L = fmaf(f, ml.y, L);
       acc[0] = fmaf(f, x.x, acc[0]); acc[1] = fmaf(f, x.y, acc[1]); acc[2] = fmaf(f, x.z, acc[2]); acc[3] = fmaf(f, x.w, acc[3]);
       acc[4] = fmaf(f, y.x, acc[4]); acc[5] = fmaf(f, y.y, acc[5]); acc[6] = fmaf(f, y.z, acc[6]); acc[7] = fmaf(f, y.w, acc[7]);
     }

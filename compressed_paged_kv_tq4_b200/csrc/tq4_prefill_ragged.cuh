@@ -1319,40 +1319,51 @@ __global__ void __launch_bounds__(256) ragged_combine_kernel(const RaggedParams 
   const int b = int(blockIdx.x) + 1, row = threadIdx.x;
   pdl_wait();
   pdl_launch_dependents();
+  // pairs b, b + 1, ... hold the rest of the item, as their first stretch, while their shares begin inside it: a
+  // warp looks at 32 of them at once (one after the other, the dependent loads took 10 us)
+  const int lane = threadIdx.x & 31;
   const int n_pairs = p.head->n_pairs;
+  const RgStart prev = p.starts[min(b, p.max_pairs) - 1], at = p.starts[min(b + lane, p.max_pairs - 1)];
   if (b >= n_pairs) return;
-  const RgStart me = p.starts[b], prev = p.starts[b - 1];
+  RgStart me;
+  me.head = __shfl_sync(0xffffffffu, at.head, 0);
+  me.blk = __shfl_sync(0xffffffffu, at.blk, 0);
+  me.tile = __shfl_sync(0xffffffffu, at.tile, 0);
   if (me.tile == 0) return;                                                        // no item is cut here
-  if (prev.head == me.head && prev.blk == me.blk && prev.tile > 0) return;         // not its first cut
-  const int part0 = 2 * (b - 1) + (prev.head == me.head && prev.blk == me.blk ? 0 : 1);
+  const bool same = prev.head == me.head && prev.blk == me.blk;
+  if (same && prev.tile > 0) return;                                               // not its first cut
+  const int64_t part0 = 2 * (b - 1) + (same ? 0 : 1);
+  int run = 0;   // of those pairs
+  for (int i = b;; i += 32) {
+    const RgStart x = i == b ? at : p.starts[min(i + lane, p.max_pairs - 1)];
+    const uint32_t in = __ballot_sync(0xffffffffu, i + lane < n_pairs && x.head == me.head && x.blk == me.blk);
+    run += in == 0xffffffffu ? 32 : __ffs(~in) - 1;
+    if (in != 0xffffffffu) break;
+  }
   const RgReq rq = p.req[p.blk_req[me.blk]];
   const int rb = me.blk - rq.blk0, n_rows = min(256, 6 * rq.n_new - 256 * rb);
   if (row >= n_rows) return;
-  // pairs b, b + 1, ... hold the rest of the item, as their first stretch, while their shares begin inside it
-  auto more = [&](int i) {
-    if (i >= n_pairs) return false;
-    const RgStart s = p.starts[i];
-    return s.head == me.head && s.blk == me.blk;
-  };
-  float M = p.pml[int64_t(part0) * 256 + row].x;
-  for (int i = b; more(i); ++i) M = fmaxf(M, p.pml[int64_t(2 * i) * 256 + row].x);
+  float M = p.pml[part0 * 256 + row].x;
+#pragma unroll 4
+  for (int i = 0; i < run; ++i) M = fmaxf(M, p.pml[int64_t(2 * (b + i)) * 256 + row].x);
   float L = 0.f, o[16];
 #pragma unroll
   for (int x = 0; x < 16; ++x) o[x] = 0.f;
-  for (int i = b - 1; i < b || more(i); ++i) {
-    const int64_t part = i < b ? part0 : 2 * i;
+#pragma unroll 2
+  for (int i = -1; i < run; ++i) {
+    const int64_t part = i < 0 ? part0 : 2 * (b + i);
     const float2 ml = p.pml[part * 256 + row];
-    if (ml.x == -INFINITY && ml.y == 0.f) continue;   // that stretch showed this row nothing
-    const float f = fast_exp2(ml.x - M);
-    L = fmaf(f, ml.y, L);
     const float4* src = reinterpret_cast<const float4*>(p.po) + (part * 64 + 4 * int(blockIdx.y)) * 256 + row;
+    const float4 a[4] = {src[0], src[256], src[512], src[768]};
+    const bool seen = ml.x != -INFINITY || ml.y != 0.f;   // else that stretch showed this row nothing
+    const float f = seen ? fast_exp2(ml.x - M) : 0.f;
+    L = fmaf(f, ml.y, L);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const float4 a = src[x * 256];
-      o[4 * x] = fmaf(f, a.x, o[4 * x]);
-      o[4 * x + 1] = fmaf(f, a.y, o[4 * x + 1]);
-      o[4 * x + 2] = fmaf(f, a.z, o[4 * x + 2]);
-      o[4 * x + 3] = fmaf(f, a.w, o[4 * x + 3]);
+    for (int x = 0; x < 4; ++x) {   // (such a stretch's sums are zeros)
+      o[4 * x] = fmaf(f, a[x].x, o[4 * x]);
+      o[4 * x + 1] = fmaf(f, a[x].y, o[4 * x + 1]);
+      o[4 * x + 2] = fmaf(f, a[x].z, o[4 * x + 2]);
+      o[4 * x + 3] = fmaf(f, a[x].w, o[4 * x + 3]);
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
