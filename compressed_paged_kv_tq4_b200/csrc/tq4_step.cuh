@@ -307,17 +307,18 @@ struct LaneAngles {
   int partner;
   bool active;
 };
-// false: a position outside the table (the same in every lane of the CTA)
-__device__ __forceinline__ bool load_angles(const RopeParams& p, int tok, LaneAngles& a) {
-  const int lane = threadIdx.x & 31, half = p.rot >> 1;
-  int32_t pos[3];
+// a token's positions on its axes; false: one lies outside the table (the same in every lane of the CTA)
+__device__ __forceinline__ bool load_positions(const RopeParams& p, int tok, int32_t pos[3]) {
   bool ok = true;
 #pragma unroll
   for (int x = 0; x < 3; ++x) {
     pos[x] = x < p.n_axes ? __ldg(p.pos + int64_t(x) * p.n_tok + tok) : 0;
     ok &= pos[x] >= 0 && pos[x] < p.table_len;
   }
-  if (!ok) return false;
+  return ok;
+}
+__device__ __forceinline__ void load_angles(const RopeParams& p, const int32_t pos[3], LaneAngles& a) {
+  const int lane = threadIdx.x & 31, half = p.rot >> 1;
   a.active = 8 * lane < p.rot;
   const int per = p.adjacent ? 4 : 8;      // frequencies of this lane
   const int m = half >> 3;                 // lanes per half
@@ -329,7 +330,7 @@ __device__ __forceinline__ bool load_angles(const RopeParams& p, int tok, LaneAn
     a.c[i] = 1.f;
     a.s[i] = 0.f;
   }
-  if (!a.active) return true;
+  if (!a.active) return;
   if (p.n_axes == 1) {   // consecutive entries of one row, 16 bytes at a time
     const float4* src = reinterpret_cast<const float4*>(p.table + int64_t(pos[0]) * half + f0);
 #pragma unroll
@@ -341,7 +342,7 @@ __device__ __forceinline__ bool load_angles(const RopeParams& p, int tok, LaneAn
         a.c[i + 1] = cs.z;
         a.s[i + 1] = sgn * cs.w;
       }
-    return true;
+    return;
   }
   uint32_t wa = 0;   // a lane's frequencies lie in one word
 #pragma unroll
@@ -355,7 +356,6 @@ __device__ __forceinline__ bool load_angles(const RopeParams& p, int tok, LaneAn
       a.c[i] = cs.x;
       a.s[i] = sgn * cs.y;
     }
-  return true;
 }
 __device__ __forceinline__ void rotate8(const LaneAngles& a, bool adjacent, float x[8]) {
   if (adjacent) {
@@ -389,8 +389,10 @@ __device__ __noinline__ void encode_again64(const RopeParams& p, int tok, int kv
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = raw[i];
   if (kv == 0) {
+    int32_t pos[3];
     LaneAngles a;
-    load_angles(p, tok, a);
+    load_positions(p, tok, pos);
+    load_angles(p, pos, a);
     if (p.adjacent) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -451,7 +453,10 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 3) rope_append_kernel(const _
   const float cell = g_cells[lane];
   pdl_wait();
   pdl_launch_dependents();
+  // the slot's and the positions' loads fly together, and with the rows'
   const int64_t slot = __ldg(p.slots + tok);
+  int32_t pos[3];
+  const bool pos_ok = load_positions(p, tok, pos);
   const bool adjacent = p.adjacent != 0;
   constexpr int kBatch = sizeof(T) == 2 ? kGroup : kGroup / 2;   // query rows in flight
   if (w < 4) {
@@ -461,9 +466,9 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 3) rope_append_kernel(const _
     Raw8<T> raw[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) raw[j].load(src + j * kD);
-    if (slot < 0 || slot >= int64_t(p.num_pages) * kPage) return;   // see below
+    if (slot < 0 || slot >= int64_t(p.num_pages) * kPage || !pos_ok) return;   // see below
     LaneAngles a;
-    if (!load_angles(p, tok, a)) return;
+    load_angles(p, pos, a);
 #pragma unroll
     for (int j0 = 0; j0 < kGroup; j0 += kBatch) {
       if (j0 > 0) {
@@ -490,28 +495,22 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 3) rope_append_kernel(const _
     if (w == 4 && lane == 0) record_error(p.status, TQ4_ERR_PAGE_RANGE);
     return;
   }
+  if (!pos_ok) {   // the values' warps look at the positions too, so that a bad one leaves the whole token unwritten
+    if (w == 4 && lane == 0) record_error(p.status, TQ4_ERR_SEQ);
+    return;
+  }
   float y[2][8];
   raw[0].get(y[0]);
   raw[1].get(y[1]);
   uint4 turned[2];
   if (kv == 0) {
     LaneAngles a;
-    if (!load_angles(p, tok, a)) {
-      if (w == 4 && lane == 0) record_error(p.status, TQ4_ERR_SEQ);
-      return;
-    }
+    load_angles(p, pos, a);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       rotate8(a, adjacent, y[j]);
       turned[j] = pack8_bf16(y[j]);
     }
-  } else {   // values are not rotated; their warps check the positions too, so that a bad one leaves the whole token unwritten
-    bool ok = true;
-    for (int x = 0; x < p.n_axes; ++x) {
-      const int32_t at = __ldg(p.pos + int64_t(x) * p.n_tok + tok);
-      ok &= at >= 0 && at < p.table_len;
-    }
-    if (!ok) return;
   }
   const uint32_t sb = lane_sign_bits(p.signs);
   uint8_t* page = p.pool + (slot >> 8) * kPageBytes;
