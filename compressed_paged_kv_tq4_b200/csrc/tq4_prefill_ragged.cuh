@@ -48,6 +48,11 @@
 // S = Qh Kh + Ql Kh + Qh Kl, O = Ph Vh + Pl Vh + Ph Vl, tiles of 64 positions, one stage.
 // TMEM (512 columns): S/P buffers at 0 and 128, O at 256. Every wait is bounded, as in the
 // one-request prefill.
+//
+// Measured (B200; 2,048 tokens on 32,768 positions, window 4,096, bf16): prep 27 us, attend 194 us
+// (206 GFLOP: 1,060 TFLOP/s, the tensor pipe busy 62 % of the cycles), combine 13 us with cold caches;
+// 242 us in all, the three overlapping at their ends. Eight chunks of 17 to 1,024 tokens on up to
+// 16,384: 51, 366 and 13 us.
 #pragma once
 #include "tq4_decode_q1.cuh"
 #include "tq4_prefill_tc.cuh"
@@ -221,7 +226,9 @@ __device__ __forceinline__ RgSpan rg_block_span(const RaggedParams& p, const RgR
 // --------------------------------------------------------------------------
 // prep. Every CTA scans the requests (as plan_step does); CTA 0 then lays out the work, the
 // others make rows, a warp at a time: four positions of one KV head, keys and values, or four of a
-// token's queries.
+// token's queries. Bound by instruction issue and the rows' writes together (2,048 tokens and 6,144
+// positions: 12 M instructions, 76 MB): 27 us. Two CTAs an SM, for three would spill (253 us a call
+// against 247).
 // --------------------------------------------------------------------------
 constexpr int kRgPrepThreads = 256;
 
