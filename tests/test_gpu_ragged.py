@@ -322,3 +322,98 @@ def test_a_run_of_the_step(ctx):
     exp = S.decode_attention_window(opool, tab, lens, qr[:4].view(4, 1, 24, 256).double().cpu().numpy(), window, sinks, SCALE, signs, c)
     assert_close(dec, exp)
     assert (lens == 0).any() and (lens > 0).any() and ctx.status() == tq4.TQ4_OK
+
+
+def test_a_captured_step(ctx):
+    """Plan, rotary append and windowed decode in one graph, replayed with other lengths: as the calls one by one."""
+    rng = np.random.default_rng(17)
+    n_req, max_pages, n_pages, rot = 6, 3, 20, 64
+    signs, c = I.signs(CFG), O.codebook()[0]
+    base = random_pool(rng, n_pages)
+    tab = np.full((n_req, max_pages), -1, np.int64)
+    ids = rng.permutation(n_pages)
+    tab[:, 0], free = ids[:n_req], ids[n_req:]
+    table = ctx.rope_table(1000, rot, 1e4)
+    qkv = torch.from_numpy(rng.normal(size=(n_req, 32 * 256)).astype(np.float32)).bfloat16().cuda()
+    q, k, v = qkv[:, :6144].view(n_req, 24, 256), qkv[:, 6144:7168].view(n_req, 4, 256), qkv[:, 7168:].view(n_req, 4, 256)
+    pool, dtab, past, new = torch.from_numpy(base).cuda(), _i32(tab), _i32(np.zeros(n_req)), _i32(np.ones(n_req))
+    dfree, out = _i32(free), torch.zeros((n_req, 1, 24, 256), dtype=torch.float32, device="cuda")
+    cu, lens, taken = _i32(np.zeros(n_req + 1)), _i32(np.zeros(n_req)), _i32([0])
+    pos, slot, qr = _i32(np.zeros(n_req)), torch.zeros(n_req, dtype=torch.int64, device="cuda"), torch.zeros((n_req, 24, 256), dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        ctx.plan_step(past, new, dfree, dtab, n_pages, cu_tok=cu, seq_lens=lens, tok_pos=pos, tok_slot=slot, taken=taken)
+        ctx.rope_append(pool, q, k, v, pos, table, slot, q_out=qr)
+        ctx.decode_attention_window(pool, qr.view(n_req, 1, 24, 256), dtab, lens, 100, 2, SCALE, out=out)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for lens_now in ([0, 5, 255, 256, 100, 30], [200, 1, 2, 3, 4, 250]):
+        past.copy_(torch.tensor(lens_now, dtype=torch.int32))
+        dtab.copy_(_i32(tab))
+        pool.copy_(torch.from_numpy(base))
+        g.replay()
+        torch.cuda.synchronize()
+        assert ctx.status() == tq4.TQ4_OK
+        etab, _, elens, epos, eslot, _, _ = S.plan_step(lens_now, [1] * n_req, free, tab, n_pages, n_req)
+        assert dtab.tolist() == etab.tolist() and lens.tolist() == elens.tolist() and slot.tolist() == eslot.tolist()
+        cs = table.cpu().double().numpy()[epos]
+        opool = base.copy()
+        S.store(opool, eslot, S.rope_turn(k.double().cpu().numpy(), cs[..., 0], cs[..., 1], False), v.double().cpu().numpy(), signs, c)
+        assert np.array_equal(pool.cpu().numpy(), opool)
+        exp = S.decode_attention_window(opool, etab, elens, qr.double().cpu().numpy()[:, None], 100, 2, SCALE, signs, c)
+        assert_close(out, exp)
+
+
+def test_two_streams_at_once(ctx):
+    """Windowed decodes and ragged prefills on two streams, each with its workspace: as one after the other."""
+    rng, lens, tab, pool, cu, q, k, v = _case([700, 90], [150, 40], seed=18)
+    dev = [torch.from_numpy(pool).cuda(), q.cuda(), k.cuda(), v.cuda(), _i32(cu), _i32(lens), _i32(tab)]
+    rng, lens2, tab2, pool2, _, q2, _, _ = _case([int(x) for x in np.linspace(1, 2600, 50)], [1] * 50, seed=19)
+    dec = [torch.from_numpy(pool2).cuda(), q2.cuda().view(50, 1, 24, 256), _i32(tab2), _i32(lens2)]
+    one = [ctx.prefill_attention_ragged(*dev, 300, 4, SCALE), ctx.decode_attention_window(*dec, 2500, 3, SCALE)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(5):
+        got.append((ctx.prefill_attention_ragged(*dev, 300, 4, SCALE, stream=streams[0]),
+                    ctx.decode_attention_window(*dec, 2500, 3, SCALE, stream=streams[1])))
+    torch.cuda.synchronize()
+    assert ctx.status() == tq4.TQ4_OK
+    for a, b in got:
+        assert torch.equal(a, one[0]) and torch.equal(b, one[1])
+
+
+def test_thousands_of_requests(ctx):
+    """More requests and row blocks than the prep keeps in shared memory; most requests idle."""
+    rng = np.random.default_rng(20)
+    new = np.zeros(3000, np.int64)
+    new[rng.permutation(3000)[:900]] = rng.integers(1, 4, 900)
+    past = np.where(new > 0, rng.integers(0, 40, 3000), 0)
+    _run(ctx, past.tolist(), new.tolist(), 20, 2, torch.bfloat16, seed=20)
+
+
+def test_pages_past_four_gigabytes(ctx):
+    """The same requests on pages at the start of a pool and at the end of one of 4.4 GB: the same results."""
+    rng, lens, tab, pool, cu, q, k, v = _case([300, 40], [20, 9], seed=21)
+    pages, far = pool.size // O.PAGE_BYTES, 16_400
+    small = torch.from_numpy(pool).cuda()
+    big = tq4.Context.new_pool(far + pages)
+    big[far * O.PAGE_BYTES:] = small
+    ftab = np.where(tab >= 0, tab + far, -1)
+    rows = [q.cuda(), k.cuda(), v.cuda(), _i32(cu), _i32(lens)]
+    slots = torch.arange(29, device="cuda")
+    table, pos = ctx.rope_table(100, 64, 1e4), _i32(np.arange(29))
+    res = []
+    for mem, t, base in ((small, tab, 0), (big, ftab, far * 256)):
+        a = ctx.prefill_attention_ragged(mem, *rows, _i32(t), 200, 3, SCALE)
+        b = ctx.decode_attention_window(mem, rows[0][:4].view(2, 2, 24, 256), _i32(t), rows[4], 200, 3, SCALE)
+        ctx.rope_append(mem, *rows[:3], pos, table, slots + base)
+        res.append((a, b, *ctx.reconstruct_slots(mem, slots + base)))
+    torch.cuda.synchronize()
+    assert ctx.status() == tq4.TQ4_OK
+    for x, y in zip(*res):
+        assert torch.equal(x, y)

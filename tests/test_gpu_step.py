@@ -85,6 +85,17 @@ def test_plan_edges(ctx):
     _check_plan(ctx, [10], [0], [], np.full((1, 1), 1), 4, 0)
 
 
+def test_plan_of_the_most_requests(ctx):
+    n = tq4.PLAN_MAX_REQUESTS
+    new = np.ones(n, np.int64)
+    new[5] = 300
+    tab = np.full((n, 2), -1)
+    _check_plan(ctx, np.zeros(n, np.int64), new, np.arange(n + 1), tab, n + 1, int(new.sum()))
+    with pytest.raises(tq4.TQ4Error) as e:
+        ctx.plan_step(*(_i32(np.zeros(n + 1)) for _ in range(3)), _i32(np.zeros((n + 1, 1))), 4, max_tok=4)
+    assert e.value.code == tq4.TQ4_ERR_UNSUPPORTED
+
+
 def test_plan_leaves_other_entries_alone_and_repeats(ctx):
     tab = np.arange(24).reshape(3, 8)
     args = ([300, 512, 1], [100, 256, 254], [30, 31, 32], tab, 40, 700)

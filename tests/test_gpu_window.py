@@ -144,6 +144,15 @@ def test_a_line_of_ragged_requests(ctx, dtype, n_q, window, sinks):
     _run(ctx, [0] * 59 + [1500], n_q, window, sinks, dtype, seed=8)
 
 
+def test_a_line_of_more_requests_than_a_plan_round(ctx):
+    rng = np.random.default_rng(77)
+    lens = np.zeros(1500, np.int64)
+    lens[rng.permutation(1500)[:40]] = rng.integers(1, 700, 40)
+    lens[1499] = 2900
+    assert ctx.decode_window_workspace(1500, 1, 12, BIG, 0).numel() > 256
+    _run(ctx, [int(x) for x in lens], 1, BIG, 0, torch.float32, seed=9)
+
+
 def test_a_line_without_work(ctx):
     rng = np.random.default_rng(1)
     pool = torch.from_numpy(random_pool(rng, 2)).cuda()
