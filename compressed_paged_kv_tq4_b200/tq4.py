@@ -911,16 +911,18 @@ class Context:
                 raise ValueError("give max_tok or tok_pos")
             max_tok = tok_pos.numel()
         i32, i64 = torch.int32, torch.int64
-        if cu_tok is None:
-            cu_tok = torch.empty(n + 1, dtype=i32, device=dev)
-        if seq_lens is None:
-            seq_lens = torch.empty(n, dtype=i32, device=dev)
-        if tok_pos is None:
-            tok_pos = torch.empty(max_tok, dtype=i32, device=dev)
-        if tok_slot is None:
-            tok_slot = torch.empty(max_tok, dtype=i64, device=dev)
-        if taken is None:
-            taken = torch.empty(1, dtype=i32, device=dev)
+        if cu_tok is None or seq_lens is None or tok_pos is None or tok_slot is None or taken is None:
+            with _allocating(stream):
+                if cu_tok is None:
+                    cu_tok = torch.empty(n + 1, dtype=i32, device=dev)
+                if seq_lens is None:
+                    seq_lens = torch.empty(n, dtype=i32, device=dev)
+                if tok_pos is None:
+                    tok_pos = torch.empty(max_tok, dtype=i32, device=dev)
+                if tok_slot is None:
+                    tok_slot = torch.empty(max_tok, dtype=i64, device=dev)
+                if taken is None:
+                    taken = torch.empty(1, dtype=i32, device=dev)
         n_free, max_pages = free_pages.numel(), page_tables.shape[-1]
         _need("past_lens", past_lens, i32, (n,), dev)
         _need("new_lens", new_lens, i32, (n,), dev)
@@ -945,8 +947,9 @@ class Context:
 
     def rope_table(self, table_len, rot, base, stream=None) -> torch.Tensor:
         """{cos, sin} of pos * base^(-2 i / rot): float32 [table_len, rot / 2, 2]."""
-        table = torch.empty((table_len, rot // 2, 2), dtype=torch.float32, device=self.device)
-        _check(tq4_rope_table(self.handle, table, table_len, rot, base, stream), "tq4_rope_table")
+        with _allocating(stream):
+            table = torch.empty((table_len, rot // 2, 2), dtype=torch.float32, device=self.device)
+        _check(_lib.tq4_rope_table(self.handle, table.data_ptr(), table_len, rot, base, self._stream(stream)), "tq4_rope_table")
         return table
 
     def rope_append(self, pool, q, k, v, pos, table, slots, sections=None, interleaved=False, pairs="halves",

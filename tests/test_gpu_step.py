@@ -314,3 +314,32 @@ def test_refusals(ctx):
         ctx.plan_step(_i32([1]), _i32([1]), _i32([1]), _i32([[1]]), 0, max_tok=4)
     torch.cuda.synchronize()
     assert ctx.status() == tq4.TQ4_OK
+
+
+def test_results_on_another_stream_are_its_own(ctx):
+    """Calls on a stream of their own while the current one has still to fill memory that it has freed."""
+    rng = np.random.default_rng(43)
+    n, tokens = 300, 900
+    past, new, tab = _i32(np.zeros(n)), _i32(np.full(n, 3)), _i32(np.full((n, 1), -1))
+    free, pool = _i32(np.arange(n)), torch.zeros(n * O.PAGE_BYTES, dtype=torch.uint8, device="cuda")
+    q, k, v = (torch.from_numpy(rng.normal(size=(tokens, h, 256)).astype(np.float32)).bfloat16().cuda() for h in (24, 4, 4))
+    busy, s = torch.empty(1 << 30, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()
+
+    def run(stream):
+        table = ctx.rope_table(100, 64, 1e4, stream=stream)
+        cu, lens, pos, slot, taken = ctx.plan_step(past, new, free, tab, n, max_tok=tokens, stream=stream)
+        qr = ctx.rope_append(pool, q, k, v, pos, table, slot, stream=stream)
+        return (table, cu, lens, pos, slot, taken, qr, *ctx.reconstruct_slots(pool, slot, stream=stream))
+
+    exp = run(None)
+    torch.cuda.synchronize()
+    for stream in (s, s.cuda_stream):
+        for _ in range(50):
+            busy.fill_(1)
+        for t in exp:
+            torch.empty_like(t).fill_(77)   # freed at once, filled later
+        got = run(stream)
+        torch.cuda.synchronize()
+        assert ctx.status() == tq4.TQ4_OK
+        for a, b in zip(got, exp):
+            assert torch.equal(a, b)
