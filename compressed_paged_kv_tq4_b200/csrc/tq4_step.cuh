@@ -450,7 +450,7 @@ __device__ __noinline__ void encode_again64(const RopeParams& p, int tok, int kv
 }
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kRopeWarps, 3) rope_append_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(32 * kRopeWarps, 4) rope_append_kernel(const __grid_constant__ RopeParams p) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int tok = blockIdx.x;
   const float cell = g_cells[lane];
