@@ -112,16 +112,16 @@ def workload_config(name, world):
 # DRAM bytes (read + write) per launch of each workload's dominant kernel, from one
 # ncu capture of that workload (summarised under profiles/). The figures count only
 # while the kernel sources hash to the value they had when the counters were taken.
-MEASURED_TRAFFIC_SOURCES = "81146d84783b578fdc5f5ee647aa5ef68b3200ce0346657ec42fc5cbaafb8962"
+MEASURED_TRAFFIC_SOURCES = "f99fadbd6cb09ad6408e41411e38ede3fdb05842a47825485094656aeaa44e76"
 MEASURED_TRAFFIC = {
-    "decode_32k": 34_211_328,              # decode_q1_kernel<0,4>: 34,184,192 read + 27,136 written
-    "decode_213k_outliers": 225_408_512,   # decode_q1_kernel<0,4>: 221,967,104 read + 3,441,408 written
-    "verify_2req_229k": 225_203_456,       # decode_splitk_kernel<3,3>: 221,758,720 read + 3,444,736 written
-    "shared_prefix_8req_33k": 42_983_168,  # decode_splitk_kernel<1,6> (grouped): 42,841,600 read + 141,568 written
-    "int8_decode_32k": 68_535_040,         # decode_splitk_kernel<1,1,INT8>: 67,693,824 read + 841,216 written
-    "prefill_2k_on_32k": 202_664_192,      # prefill_tc_kernel: 101,468,672 read + 101,195,520 written (segment partials)
-    "tqb3_decode_32k": 25_801_984,         # decode_q1_kernel<0,3>: 25,801,984 read + 0 written
-    "tqb2_decode_32k": 17_408_512,         # decode_q1_kernel<0,2>: 17,408,512 read + 0 written
+    "decode_32k": 34_200_064,              # decode_q1_kernel<0,4>: 34,184,448 read + 15,616 written
+    "decode_213k_outliers": 224_923_648,   # decode_q1_kernel<0,4>: 221,936,896 read + 2,986,752 written
+    "verify_2req_229k": 224_685_312,       # decode_splitk_kernel<3,3>: 221,703,680 read + 2,981,632 written
+    "shared_prefix_8req_33k": 42_945_024,  # decode_splitk_kernel<1,6> (grouped): 42,846,720 read + 98,304 written
+    "int8_decode_32k": 68_526_336,         # decode_splitk_kernel<1,1,INT8>: 67,694,080 read + 832,256 written
+    "prefill_2k_on_32k": 202_362_368,      # prefill_tc_kernel: 102,199,040 read + 100,163,328 written (segment partials)
+    "tqb3_decode_32k": 25_801_472,         # decode_q1_kernel<0,3>: 25,801,472 read + 0 written
+    "tqb2_decode_32k": 17_408_768,         # decode_q1_kernel<0,2>: 17,408,768 read + 0 written
 }
 
 

@@ -22,7 +22,7 @@
 // Measured (B200): one request, window 4,096, clusters: 13.4 us a call (latency: the launch, the
 // table, two rounds of tiles, the merge). 64 requests of 300 to 32,768 positions, bf16: 62.8 us a
 // call on the line (59 us this kernel, 171 MB: 2.9 TB/s) against 73.9 with one CTA per item; 16
-// requests with four tokens, window 8,192, fp32: 107 us against 138. Bound by instruction issue at
+// requests with four tokens, window 8,192, fp32: 114 us (138 with one CTA per item, before the chains below). Bound by instruction issue at
 // two warps a scheduler (1,100 instructions per tile, 0.42 a cycle): the registers and shared
 // memory of eight warps fill an SM.
 //
@@ -36,7 +36,8 @@
 // single f16 values (each off by at most 2^-11 relative; in the result these are
 // ~6e-4 next to the 1.7e-3 of the bf16 rounding itself, both root mean square). fp32
 // results (kExact): f16 hi + lo pairs, S = C q'hi + C q'lo + R q'hi, O = C Phi + C Plo
-// + R Phi, with the weights at most 1 so that their lo parts keep their digits.
+// + R Phi, with the weights at most 1 so that their lo parts keep their digits. Against 64 bits, 2-norm:
+// 8e-7 with one or two tokens, 2.7e-6 with more (4.2e-6 with every product in one chain a row, 6 % faster).
 #pragma once
 #include "tq4_decode_q1.cuh"
 
@@ -403,6 +404,9 @@ __global__ void __launch_bounds__(kQ1Threads, 1)
     const int c = tile_pos(k);
 
     // ------------------------------------------------------------ scores of 32 positions
+    // The tensor cores cut off what a sum cannot hold, always towards zero, so a long chain of products is off by
+    // its length: the lo products (two of three) have sums of their own (three n-tiles: no registers for them).
+    constexpr bool kLo = kExact && NT < 3;
     float s[2][NT][4];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -411,6 +415,13 @@ __global__ void __launch_bounds__(kQ1Threads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[j][n][i] = 0.f;
     if (have) {
+      float s_lo[kLo ? 2 : 1][NT][4];
+#pragma unroll
+      for (int j = 0; j < (kLo ? 2 : 1); ++j)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s_lo[j][n][i] = 0.f;
       uint4 ka[2], kb4[2], kc[2], kd[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -458,11 +469,19 @@ __global__ void __launch_bounds__(kQ1Threads, 1)
             const uint32_t q0 = kPair ? qb[n][x] : qh[kPair ? 0 : kk][0], q1 = kPair ? qb[n][x + 1] : qh[kPair ? 0 : kk][1];
             mma_16816(s[j][n], a0, a1, a2, a3, q0, q1);
             if constexpr (kExact) {
-              mma_16816(s[j][n], a0, a1, a2, a3, ql[n][x], ql[n][x + 1]);
-              mma_16816(s[j][n], r0, r1, r2, r3, q0, q1);
+              mma_16816(kLo ? s_lo[j][n] : s[j][n], a0, a1, a2, a3, ql[n][x], ql[n][x + 1]);
+              mma_16816(kLo ? s_lo[j][n] : s[j][n], r0, r1, r2, r3, q0, q1);
             }
           }
         }
+      }
+      if constexpr (kLo) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[j][n][i] += s_lo[j][n][i];
       }
     }
 
@@ -621,10 +640,15 @@ __global__ void __launch_bounds__(kQ1Threads, 1)
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              mma_16816(o[4 * q + kb][n], a0, a1, a2, a3, ph[j][n][0], ph[j][n][1]);
-              if constexpr (kExact) {
-                mma_16816(o[4 * q + kb][n], a0, a1, a2, a3, pl[j][n][0], pl[j][n][1]);
-                mma_16816(o[4 * q + kb][n], r0, r1, r2, r3, ph[j][n][0], ph[j][n][1]);
+              if constexpr (kExact) {   // chains of three products, added up by rounded additions (see the scores)
+                float u[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_16816(u, a0, a1, a2, a3, pl[j][n][0], pl[j][n][1]);
+                mma_16816(u, r0, r1, r2, r3, ph[j][n][0], ph[j][n][1]);
+                mma_16816(u, a0, a1, a2, a3, ph[j][n][0], ph[j][n][1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[4 * q + kb][n][i] += u[i];
+              } else {
+                mma_16816(o[4 * q + kb][n], a0, a1, a2, a3, ph[j][n][0], ph[j][n][1]);
               }
             }
           }

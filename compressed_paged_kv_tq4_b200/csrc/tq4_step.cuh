@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float2* table, int64_t 
 //
 // One CTA of 8 warps per token: warps 0-3 six query heads each, 4-5 two keys, 6-7 two
 // values, so that all end together; a row's loads go out before the position's. Bound by
-// instruction issue (6,400 a token) beside the loads' latency at 2,048 bf16 tokens, 31 us, and by
-// memory at 8,191 fp32 tokens, 89 us (393 MB, 4.4 TB/s).
+// instruction issue (6,400 a token) beside the loads' latency at 2,048 bf16 tokens, 29 us, and by
+// memory at 8,191 fp32 tokens, 82 us (393 MB, 4.8 TB/s); with three CTAs an SM 31 and 89.
 // --------------------------------------------------------------------------
 constexpr int kRopeWarps = 8;
 constexpr float kRopeNear = 1.25e-6f;   // coordinates closer to a boundary are decided in 64 bits
